@@ -388,6 +388,103 @@ TTT_API int ttt_mlp_momentum_decode(const void *q, const void *k, const void *v,
                                     float ln_eps, int B, int H, int d, int hidden, int b, int pos,
                                     float *z, void *stream);
 
+/*
+ * Linear attention with a decay for each head, over whole sequences: TTT with a
+ * linear f and batch gradient descent is linear attention (§03.8); the decay is
+ * the forget factor of the Titans article (§二.1(2)), held constant per head.  With
+ * gamma_h = exp(log_decay[h]) and the state S [d][d] of each (batch, head):
+ *   S_t = gamma_h S_{t-1} + k_t^T v_t,   z_t = scale * q_t S_t,   S_{-1} = S0.
+ *   Q, K, V    [B][H][T][d] (qkv_dtype)
+ *   log_decay  [H] fp32: natural logarithms of the decay factors, <= 0 (0: no
+ *              decay; -infinity: nothing is kept).  The decay is a constant of the
+ *              layer: there is no gradient with respect to it.
+ *   S0         [B][H][d][d] fp32 or NULL (zero): the state to continue from.
+ *   lengths    [B] int or NULL: sequence b has the tokens 0 .. lengths[b] - 1
+ *              (values outside [0, T] count as the nearer end); NULL: all T.  Rows
+ *              behind a sequence's end are not used, whatever they hold; their
+ *              rows of Z are zeros.
+ * Outputs: Z [B][H][T][d] in the type of Q, K, V, rounded once from fp32 (the
+ * layer's next product takes that type; what is carried on stays fp32); S_out
+ * [B][H][d][d] fp32 or NULL: the state after each sequence's last token (S0, or
+ * zero, for an empty one).
+ * d = 64 (else TTT_ERR_UNSUPPORTED), any T >= 0; B*H*T*d < 2^40.  scale must be
+ * finite.  Arithmetic: chunks of masked products.  With fp32 inputs fp32 FMAs.
+ *
+ * workspace: DEVICE memory owned by the caller, 16-byte aligned, at least
+ * ttt_linear_attn_workspace_bytes(B, H, T, d, 0) bytes (often 0, then NULL is
+ * allowed): with few (batch, head) units a sequence is cut into segments whose
+ * states lie there.  It needs no clearing; calls ordered on one stream may share
+ * it, calls that may overlap (other streams, graphs that replay side by side) not.
+ * Errors as for the forward entry points; TTT_ERR_ARG also for a scale that is not
+ * finite and a workspace that is null or too small.
+ */
+TTT_API int ttt_linear_attn_fwd(const void *Q, const void *K, const void *V, int qkv_dtype,
+                                const float *log_decay, const float *S0, const int *lengths,
+                                float scale, int B, int H, int T, int d, void *Z, float *S_out,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace that ttt_linear_attn_fwd (backward = 0) or
+ * ttt_linear_attn_bwd (backward = 1) needs; 0 for invalid sizes too. */
+TTT_API size_t ttt_linear_attn_workspace_bytes(int B, int H, int T, int d, int backward);
+
+/*
+ * Backward pass of ttt_linear_attn_fwd: the gradients of L = <dZ, Z> + <dS_T, S_out>.
+ * With G_t the gradient of S_t:
+ *   G_t = gamma G_{t+1} + scale q_t^T dz_t  (the last token: dS_T in place of gamma G_{t+1}),
+ *   dq_t = scale dz_t S_t^T,  dk_t = v_t G_t^T,  dv_t = k_t G_t,  dS0 = gamma G_0.
+ * Inputs as for the forward, plus dZ [B][H][T][d] (qkv_dtype) and dS_T [B][H][d][d]
+ * fp32 or NULL (zero).  Outputs: dQ, dK, dV [B][H][T][d] in the type of Q, K, V,
+ * rounded once from fp32, zeros behind the ends; dS0 [B][H][d][d] fp32 or NULL
+ * (dS_T for an empty sequence).  The states are recomputed from Q, K, V: nothing of
+ * the forward is kept.  workspace as for the forward (backward = 1).
+ */
+TTT_API int ttt_linear_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype,
+                                const float *log_decay, const float *S0, const int *lengths,
+                                float scale, const void *dZ, const float *dS_T, int B, int H, int T,
+                                int d, void *dQ, void *dK, void *dV, float *dS0, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * The recurrent step of ttt_linear_attn_fwd for one token per (batch, head) and call:
+ *   S <- gamma S + k^T v,  z = scale q S.
+ *   q, k, v [B][H][d] (qkv_dtype), S [B][H][d][d] fp32 in/out, z [B][H][d] (qkv_dtype).
+ * Run over a sequence from S = S0 the calls give the forward's Z and S_out (to
+ * rounding).  rotary_dim > 0: q and k are turned first (not rounded in between) at
+ * positions [B] int by the plan inv_freq, rotary_dim, interleaved, mscale of
+ * ttt_rope; rotary_dim = 0: positions and inv_freq are ignored.  S and z must not
+ * overlap each other or the inputs.  Errors as for the forward entry points.
+ */
+TTT_API int ttt_linear_attn_decode(const void *q, const void *k, const void *v, int qkv_dtype,
+                                   const float *log_decay, float scale, float *S,
+                                   const int *positions, const float *inv_freq, int rotary_dim,
+                                   int interleaved, float mscale, int B, int H, int d, void *z,
+                                   void *stream);
+
+/*
+ * Rotary positions on Q and K (the pages take Q, K already projected and turned;
+ * this is the step before every entry point over sequences), and the layout these
+ * want.  The leading rotary_dim values of each row form pairs i = 0 ..
+ * rotary_dim / 2 - 1: values (i, i + rotary_dim / 2), or with interleaved = 1 values
+ * (2i, 2i + 1).  A token at position p has its pairs (x, y) turned by p inv_freq[i]:
+ *   (x, y) -> mscale (x cos - y sin, x sin + y cos);
+ * the row's other values are copied.  inverse = 1 turns back (sin -> -sin), which
+ * with the same mscale is the gradient of the forward turn.
+ *   Q, K         rows of d values (dtype) at strides q_strides / k_strides = {batch,
+ *                head, token} in values (host arrays of three; NULL: dense
+ *                [B][H][T][d]), not negative; every row on a 16-byte boundary (else
+ *                TTT_ERR_ALIGN).  Hq and Hk heads; with 0 heads its pointers and
+ *                strides are ignored.
+ *   positions    [B][T] int, any value, or NULL: first_position + t
+ *   inv_freq     [rotary_dim / 2] fp32; the angle is their exact product
+ *   Q_out, K_out [B][H][T][d] dense (dtype), rounded once
+ * d = 64; rotary_dim even, 0 .. d.  Errors as for the forward entry points.
+ */
+TTT_API int ttt_rope(const void *Q, const void *K, int dtype, const int *positions,
+                     int first_position, const float *inv_freq, int rotary_dim, int interleaved,
+                     float mscale, int inverse, int B, int Hq, int Hk, int T, int d,
+                     const long long *q_strides, const long long *k_strides, void *Q_out,
+                     void *K_out, void *stream);
+
 /* Static English text for a ttt_status value (never NULL). */
 TTT_API const char *ttt_status_string(int status);
 

@@ -1,6 +1,7 @@
 """TTT layers (mini-batch TTT) on NVIDIA B200, sm_100a: the dual-form forward of
 TTT-Linear, TTT-Linear + LN and TTT-MLP, its backward (TTT-Linear, + LN), the
-primal-form decode step, and the momentum and decay (Titans-style) update.
+primal-form decode step, and the momentum and decay (Titans-style) update; linear
+attention with a decay for each head (forward, backward, decode) and rotary positions.
 
 The computation lives in ``libttt.so`` (C ABI in ``include/ttt.h``); the
 functions below are its Python binding over torch CUDA tensors.  ``inputs``
@@ -19,7 +20,9 @@ def __getattr__(name):
                 "ttt_linear_momentum_decode", "ttt_linear_ln_momentum_decode",
                 "ttt_mlp_momentum_decode", "ttt_linear_bwd", "ttt_linear_momentum_fwd",
                 "ttt_linear_ln_bwd_noalloc", "ttt_mlp_bwd",
-                "ttt_mlp_momentum_fwd", "ttt_fwd_host", "fwd_host_workspace_bytes"):
+                "ttt_mlp_momentum_fwd", "ttt_fwd_host", "fwd_host_workspace_bytes",
+                "ttt_linear_attn_fwd", "ttt_linear_attn_bwd", "ttt_linear_attn_decode",
+                "linear_attn_workspace_bytes", "ttt_rope", "Rope", "rope_frequencies"):
         from . import ttt
         return getattr(ttt, name)
     raise AttributeError(name)

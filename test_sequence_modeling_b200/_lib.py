@@ -53,6 +53,15 @@ SIGNATURES = {
                                      _fp, _fp, _f, _i, _i, _i, _i, _i, _i, _fp, _vp]),
     "ttt_mlp_decode": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _fp, _fp, _fp, _fp, _fp, _f, _i, _i, _i, _i,
                             _i, _i, _fp, _vp]),
+    "ttt_linear_attn_fwd": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _vp, _f, _i, _i, _i, _i, _vp, _fp, _vp,
+                                 ctypes.c_size_t, _vp]),
+    "ttt_linear_attn_workspace_bytes": (ctypes.c_size_t, [_i, _i, _i, _i, _i]),
+    "ttt_linear_attn_bwd": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _vp, _f, _vp, _fp, _i, _i, _i, _i, _vp, _vp,
+                                 _vp, _fp, _vp, ctypes.c_size_t, _vp]),
+    "ttt_linear_attn_decode": (_i, [_vp, _vp, _vp, _i, _fp, _f, _fp, _vp, _fp, _i, _i, _f, _i, _i, _i, _vp,
+                                    _vp]),
+    "ttt_rope": (_i, [_vp, _vp, _i, _vp, _i, _fp, _i, _i, _f, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp,
+                      _vp]),
     "ttt_fwd_host_workspace_bytes": (ctypes.c_size_t, [_i, _i, _i, _i, _i, _i, _i]),
     "ttt_fwd_host": (_i, [_i, _vp, _vp, _vp, _i, _fp, _fp, _fp, _fp, _fp, _f, _i, _i, _i, _i, _i, _i,
                           _fp, _fp, _fp, _vp, ctypes.c_size_t, _i, _vp]),

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdint>
 #include <algorithm>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 #include <cuda.h>
@@ -19,8 +20,10 @@
 #include "backward.cuh"
 #include "backward_mlp.cuh"
 #include "decode.cuh"
+#include "linear_attn.cuh"
 #include "momentum.cuh"
 #include "momentum_mlp.cuh"
+#include "rope.cuh"
 #include "simt.cuh"
 #include "tc_linear.cuh"
 #include "tc_momentum.cuh"
@@ -30,6 +33,8 @@ namespace simt = ttt::simt;
 namespace tc = ttt::tc;
 namespace tcmlp = ttt::tcmlp;
 namespace decode = ttt::decode;
+namespace lattn = ttt::lattn;
+namespace rope = ttt::rope;
 namespace bwd = ttt::bwd;
 namespace bwdmlp = ttt::bwdmlp;
 namespace mom = ttt::mom;
@@ -703,6 +708,265 @@ int run_mlp_momentum_fwd(const void *Q, const void *K, const void *V, int qkv_dt
   return TTT_OK;
 }
 
+// ---- linear attention with a decay for each head, rotary positions --------------------
+
+// The pointer rules of every entry point on a call's buffers: required ones non-null, all
+// 16-byte aligned, no output over an input or another output (empty buffers are free).
+struct Buffer {
+  const void *p;
+  size_t bytes;
+  bool required;
+};
+int check_buffers(std::initializer_list<Buffer> ins, std::initializer_list<Buffer> outs) {
+  for (const auto *list : {&ins, &outs})
+    for (const Buffer &b : *list)
+      if (b.required && !b.p) return TTT_ERR_ARG;
+  for (const auto *list : {&ins, &outs})
+    for (const Buffer &b : *list)
+      if (b.p && !aligned16(b.p)) return TTT_ERR_ALIGN;
+  auto range = [](const Buffer &b) { return range_of(b.p, b.p ? b.bytes : 0); };
+  auto clash = [&](const Buffer &a, const Buffer &b) {
+    return a.p && b.p && a.bytes && b.bytes && overlap(range(a), range(b));
+  };
+  for (const Buffer *o = outs.begin(); o != outs.end(); ++o) {
+    for (const Buffer &i : ins)
+      if (clash(*o, i)) return TTT_ERR_ARG;
+    for (const Buffer *o2 = o + 1; o2 != outs.end(); ++o2)
+      if (clash(*o, *o2)) return TTT_ERR_ARG;
+  }
+  return TTT_OK;
+}
+
+// How a sequence is cut.  With units (batch x heads) enough for every SM each one runs its
+// sequence alone; with fewer, the sequences are cut into segments of whole chunks that run side
+// by side, which costs a pass over half of the inputs for the segments' own states.
+struct AttnPlan {
+  int seg_len, nseg;
+  size_t slots_bytes;  // one set of segment states
+};
+constexpr int ATTN_SMS = 148;          // SMs of a B200: the workspace size does not ask a device
+constexpr int ATTN_SEG_ALIGN = 128;    // tokens: whole chunks of every kernel
+constexpr int ATTN_SEG_MIN = 512;      // tokens a segment at least
+AttnPlan attn_plan(long long units, int T) {
+  AttnPlan a{T > 0 ? T : 1, 1, 0};
+  if (units >= ATTN_SMS || units == 0 || T <= ATTN_SEG_MIN) return a;
+  const long long want = std::min<long long>(2 * ATTN_SMS / units, (T + ATTN_SEG_MIN - 1) / ATTN_SEG_MIN);
+  if (want < 2) return a;
+  const long long len = (T + want - 1) / want;
+  a.seg_len = (int)((len + ATTN_SEG_ALIGN - 1) / ATTN_SEG_ALIGN * ATTN_SEG_ALIGN);
+  a.nseg = (T + a.seg_len - 1) / a.seg_len;
+  a.slots_bytes = a.nseg > 1 ? (size_t)units * a.nseg * lattn::D * lattn::D * 4 : 0;
+  return a;
+}
+
+template <typename KernelT, typename ParamsT>
+int launch_attn(KernelT kernel, long long grid, int threads, size_t smem, cudaStream_t s, const ParamsT &p) {
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return TTT_ERR_CUDA;
+  kernel<<<(unsigned)grid, threads, smem, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return TTT_OK;
+}
+
+// One pass of lattn::attn_kernel over all units.
+int attn_pass(bool bf16, bool reverse, long long units, const lattn::Params &p, cudaStream_t s) {
+  const long long grid = units * p.nseg;
+  auto kernel = bf16 ? (reverse ? lattn::attn_kernel<__nv_bfloat16, true> : lattn::attn_kernel<__nv_bfloat16, false>)
+                     : (reverse ? lattn::attn_kernel<float, true> : lattn::attn_kernel<float, false>);
+  return launch_attn(kernel, grid, lattn::THREADS, lattn::SMEM_BYTES, s, p);
+}
+
+// The states that the segments start from, into `slots`: the segments' own states, then the scan.
+int attn_segment_states(bool bf16, bool reverse, long long units, const AttnPlan &plan, const void *Y, const void *W,
+                        float e, const float *log_decay, const int *lengths, const float *C0, int H, int T,
+                        float *slots, cudaStream_t s) {
+  lattn::Params p{Y, Y, W, log_decay, lengths, nullptr, 0, false, false, 0.f, 0.f, e, nullptr, slots, true,
+                  H, T, plan.seg_len, plan.nseg};
+  int st = attn_pass(bf16, reverse, units, p, s);
+  if (st != TTT_OK) return st;
+  lattn::ScanParams sp{slots, C0, log_decay, lengths, H, T, plan.seg_len, plan.nseg};
+  return launch_attn(reverse ? lattn::scan_kernel<true> : lattn::scan_kernel<false>, units * 4, lattn::SCAN_THREADS, 0,
+                     s, sp);
+}
+
+// Sizes shared by the linear attention entry points over sequences.
+int check_attn_sizes(int qkv_dtype, float scale, int B, int H, int T, int d) {
+  if (qkv_dtype != TTT_F32 && qkv_dtype != TTT_BF16) return TTT_ERR_ARG;
+  if (B < 0 || H < 0 || T < 0 || d <= 0 || !std::isfinite(scale)) return TTT_ERR_ARG;
+  if (d != lattn::D) return TTT_ERR_UNSUPPORTED;
+  const long long units = (long long)B * H;
+  // Segments and the scan's four CTAs a unit multiply the grid.
+  if (units > 0x1fffffffLL || (unsigned __int128)units * (unsigned)T * (unsigned)d >= (1ULL << 40)) return TTT_ERR_UNSUPPORTED;
+  return TTT_OK;
+}
+
+int run_attn_fwd(const void *Q, const void *K, const void *V, int qkv_dtype, const float *log_decay, const float *S0,
+                 const int *lengths, float scale, int B, int H, int T, int d, void *Z, float *S_out, void *workspace,
+                 size_t workspace_bytes, void *stream) {
+  int st = check_attn_sizes(qkv_dtype, scale, B, H, T, d);
+  if (st != TTT_OK) return st;
+  const long long units = (long long)B * H;
+  if (units == 0) return TTT_OK;
+  const bool tok = T > 0, bf16 = qkv_dtype == TTT_BF16;
+  const size_t xb = (size_t)units * T * d * (bf16 ? 2 : 4), sb = (size_t)units * d * d * 4;
+  const AttnPlan plan = attn_plan(units, T);
+  if (plan.slots_bytes && (!workspace || workspace_bytes < plan.slots_bytes)) return TTT_ERR_ARG;
+  st = check_buffers({{Q, xb, tok}, {K, xb, tok}, {V, xb, tok}, {log_decay, (size_t)H * 4, true}, {S0, sb, false},
+                      {lengths, (size_t)B * 4, false}},
+                     {{Z, xb, tok}, {S_out, sb, false}, {plan.slots_bytes ? workspace : nullptr, plan.slots_bytes, false}});
+  if (st != TTT_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float *slots = static_cast<float *>(workspace);
+  const bool cut = plan.nseg > 1;
+  if (cut) {
+    st = attn_segment_states(bf16, false, units, plan, K, V, 1.f, log_decay, lengths, S0, H, T, slots, s);
+    if (st != TTT_OK) return st;
+  }
+  lattn::Params p{Q, K, V, log_decay, lengths, cut ? slots : S0, (long long)(cut ? plan.nseg : 1) * d * d, cut, false,
+                  scale, scale, 1.f, Z, S_out, false, H, T, plan.seg_len, plan.nseg};
+  return attn_pass(bf16, false, units, p, s);
+}
+
+int run_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype, const float *log_decay, const float *S0,
+                 const int *lengths, float scale, const void *dZ, const float *dS_T, int B, int H, int T, int d,
+                 void *dQ, void *dK, void *dV, float *dS0, void *workspace, size_t workspace_bytes, void *stream) {
+  int st = check_attn_sizes(qkv_dtype, scale, B, H, T, d);
+  if (st != TTT_OK) return st;
+  const long long units = (long long)B * H;
+  if (units == 0) return TTT_OK;
+  const bool tok = T > 0, bf16 = qkv_dtype == TTT_BF16;
+  const size_t xb = (size_t)units * T * d * (bf16 ? 2 : 4), sb = (size_t)units * d * d * 4;
+  const AttnPlan plan = attn_plan(units, T);
+  const size_t wb = 2 * plan.slots_bytes;
+  if (wb && (!workspace || workspace_bytes < wb)) return TTT_ERR_ARG;
+  st = check_buffers({{Q, xb, tok}, {K, xb, tok}, {V, xb, tok}, {dZ, xb, tok}, {log_decay, (size_t)H * 4, true},
+                      {S0, sb, false}, {dS_T, sb, false}, {lengths, (size_t)B * 4, false}},
+                     {{dQ, xb, tok}, {dK, xb, tok}, {dV, xb, tok}, {dS0, sb, false}, {wb ? workspace : nullptr, wb, false}});
+  if (st != TTT_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float *slots_s = static_cast<float *>(workspace), *slots_g = slots_s;
+  const bool cut = plan.nseg > 1;
+  if (cut) {
+    slots_g = slots_s + plan.slots_bytes / 4;
+    st = attn_segment_states(bf16, false, units, plan, K, V, 1.f, log_decay, lengths, S0, H, T, slots_s, s);
+    if (st != TTT_OK) return st;
+    st = attn_segment_states(bf16, true, units, plan, Q, dZ, scale, log_decay, lengths, dS_T, H, T, slots_g, s);
+    if (st != TTT_OK) return st;
+  }
+  const float *Cs = cut ? slots_s : S0, *Cg = cut ? slots_g : dS_T;
+  const long long stride = (long long)(cut ? plan.nseg : 1) * d * d;
+  lattn::Params pq{dZ, V, K, log_decay, lengths, Cs, stride, cut, true, scale, scale, 1.f, dQ, nullptr, false,
+                   H, T, plan.seg_len, plan.nseg};
+  lattn::Params pk{V, dZ, Q, log_decay, lengths, Cg, stride, cut, true, scale, 1.f, scale, dK, nullptr, false,
+                   H, T, plan.seg_len, plan.nseg};
+  lattn::Params pv{K, Q, dZ, log_decay, lengths, Cg, stride, cut, false, scale, 1.f, scale, dV, dS0, false,
+                   H, T, plan.seg_len, plan.nseg};
+  if (tok) {
+    if ((st = attn_pass(bf16, false, units, pq, s)) != TTT_OK) return st;
+    if ((st = attn_pass(bf16, true, units, pk, s)) != TTT_OK) return st;
+  }
+  return attn_pass(bf16, true, units, pv, s);
+}
+
+// The rotary arguments of a call.  TTT_OK and rotary_dim == 0: no rotation.
+int check_rope(int rotary_dim, int interleaved, float mscale, int d) {
+  if (rotary_dim < 0 || rotary_dim > d || (rotary_dim & 1)) return TTT_ERR_ARG;
+  if ((interleaved != 0 && interleaved != 1) || !std::isfinite(mscale)) return TTT_ERR_ARG;
+  return TTT_OK;
+}
+
+int run_attn_decode(const void *q, const void *k, const void *v, int qkv_dtype, const float *log_decay, float scale,
+                    float *S, const int *positions, const float *inv_freq, int rotary_dim, int interleaved,
+                    float mscale, int B, int H, int d, void *z, void *stream) {
+  int st = check_attn_sizes(qkv_dtype, scale, B, H, 1, d);
+  if (st == TTT_OK) st = check_rope(rotary_dim, interleaved, mscale, d);
+  if (st != TTT_OK) return st;
+  const long long units = (long long)B * H;
+  if (units == 0) return TTT_OK;
+  const bool bf16 = qkv_dtype == TTT_BF16, turned = rotary_dim > 0;
+  const size_t xb = (size_t)units * d * (bf16 ? 2 : 4);
+  st = check_buffers({{q, xb, true}, {k, xb, true}, {v, xb, true}, {log_decay, (size_t)H * 4, true},
+                      {turned ? positions : nullptr, (size_t)B * 4, turned},
+                      {turned ? inv_freq : nullptr, (size_t)rotary_dim * 2, turned}},
+                     {{S, (size_t)units * d * d * 4, true}, {z, xb, true}});
+  if (st != TTT_OK) return st;
+  lattn::DecodeParams p{q, k, v, log_decay, scale, S, {inv_freq, rotary_dim, interleaved != 0, mscale}, positions, H, z};
+  return launch_attn(bf16 ? lattn::decode_kernel<__nv_bfloat16> : lattn::decode_kernel<float>, units, lattn::THREADS, 0,
+                     static_cast<cudaStream_t>(stream), p);
+}
+
+// Bytes that a strided tensor of B x heads x T rows reaches over; false: a stride is negative, a row
+// does not start on a 16-byte boundary, or the reach does not fit.
+bool strided_extent(const long long *st, int B, int heads, int T, int d, size_t elt, size_t *bytes, bool *misaligned) {
+  const int n[3] = {B, heads, T};
+  unsigned __int128 reach = (unsigned)d;
+  for (int i = 0; i < 3; ++i) {
+    if (st[i] < 0) return false;
+    if (n[i] > 1 && (st[i] * (long long)elt) % 16 != 0) *misaligned = true;
+    reach += (unsigned __int128)st[i] * (unsigned)(n[i] - 1);
+  }
+  reach *= elt;
+  if (reach >= ((unsigned __int128)1 << 46)) return false;
+  *bytes = (size_t)reach;
+  return true;
+}
+
+int run_rope(const void *Q, const void *K, int dtype, const int *positions, int first_position, const float *inv_freq,
+             int rotary_dim, int interleaved, float mscale, int inverse, int B, int Hq, int Hk, int T, int d,
+             const long long *q_strides, const long long *k_strides, void *Q_out, void *K_out, void *stream) {
+  if (dtype != TTT_F32 && dtype != TTT_BF16) return TTT_ERR_ARG;
+  if (B < 0 || Hq < 0 || Hk < 0 || T < 0 || d <= 0 || (inverse != 0 && inverse != 1)) return TTT_ERR_ARG;
+  int st = check_rope(rotary_dim, interleaved, mscale, d);
+  if (st != TTT_OK) return st;
+  // Positions first .. first + T - 1 are ints.
+  if (!positions && T > 0 && (long long)first_position + T - 1 > 0x7fffffffLL) return TTT_ERR_ARG;
+  if (d != rope::D) return TTT_ERR_UNSUPPORTED;
+  const long long tokens = (long long)B * T, heads = (long long)Hq + Hk;
+  if (tokens == 0 || heads == 0) return TTT_OK;
+  if (heads > (1 << 20) || tokens >= (1LL << 34) || tokens * heads * d >= (1LL << 40))
+    return TTT_ERR_UNSUPPORTED;
+  const size_t elt = dtype == TTT_BF16 ? 2 : 4;
+  const long long dense_q[3] = {(long long)Hq * T * d, (long long)T * d, d};
+  const long long dense_k[3] = {(long long)Hk * T * d, (long long)T * d, d};
+  const long long *sq = q_strides ? q_strides : dense_q, *sk = k_strides ? k_strides : dense_k;
+  size_t qb = 0, kb = 0;
+  bool misaligned = false;
+  if (Hq > 0 && !strided_extent(sq, B, Hq, T, d, elt, &qb, &misaligned)) return TTT_ERR_ARG;
+  if (Hk > 0 && !strided_extent(sk, B, Hk, T, d, elt, &kb, &misaligned)) return TTT_ERR_ARG;
+  if (misaligned) return TTT_ERR_ALIGN;
+  const bool turned = rotary_dim > 0;
+  st = check_buffers({{Hq ? Q : nullptr, qb, Hq > 0}, {Hk ? K : nullptr, kb, Hk > 0}, {positions, (size_t)tokens * 4, false},
+                      {turned ? inv_freq : nullptr, (size_t)rotary_dim * 2, turned}},
+                     {{Hq ? Q_out : nullptr, (size_t)tokens * Hq * d * elt, Hq > 0},
+                      {Hk ? K_out : nullptr, (size_t)tokens * Hk * d * elt, Hk > 0}});
+  if (st != TTT_OK) return st;
+  rope::Params p{};
+  p.t[0] = {Q, sq[0], sq[1], sq[2], Q_out, Hq};
+  p.t[1] = {K, sk[0], sk[1], sk[2], K_out, Hk};
+  p.plan = {inv_freq, rotary_dim, interleaved != 0, mscale};
+  p.positions = positions;
+  p.first = first_position;
+  p.sin_sign = inverse ? -1.f : 1.f;
+  p.T = T;
+  p.tokens = tokens;
+  const long long tiles = (tokens + rope::TILE - 1) / rope::TILE;
+  // A tile's angles are made by every CTA that shares its heads: one CTA a tile where the tiles fill
+  // the SMs, else enough to.
+  const int vec = (int)(16 / elt), rows_a_step = rope::THREADS / (rope::D / vec / 2);
+  const long long steps = (rope::TILE * heads + rows_a_step - 1) / rows_a_step;
+  p.head_groups = (int)std::max<long long>(1, std::min<long long>(steps, 8 * ATTN_SMS / tiles));
+  const bool paired = !interleaved && (rotary_dim / 2) % vec == 0;
+  auto kernel =
+      dtype == TTT_BF16
+          ? (interleaved ? rope::rope_kernel<__nv_bfloat16, rope::INTERLEAVED>
+                         : paired ? rope::rope_kernel<__nv_bfloat16, rope::PAIRED> : rope::rope_kernel<__nv_bfloat16, rope::ANY>)
+          : (interleaved ? rope::rope_kernel<float, rope::INTERLEAVED>
+                         : paired ? rope::rope_kernel<float, rope::PAIRED> : rope::rope_kernel<float, rope::ANY>);
+  return launch_attn(kernel, tiles * p.head_groups, rope::THREADS, 0, static_cast<cudaStream_t>(stream), p);
+}
+
 int run(const Call &c) {
   const int st = validate(c);
   if (st != TTT_OK) return st;
@@ -1075,6 +1339,40 @@ int ttt_linear_ln_decode(const void *q, const void *k, const void *v, int qkv_dt
                          float *z, void *stream) {
   return run_decode(true, q, k, v, qkv_dtype, eta, W, W_base, ln_gamma, ln_beta, ln_eps, B, H, d,
                     b, pos, z, stream);
+}
+
+size_t ttt_linear_attn_workspace_bytes(int B, int H, int T, int d, int backward) {
+  if (B < 0 || H < 0 || T < 0 || check_attn_sizes(TTT_F32, 1.f, B, H, T, d) != TTT_OK) return 0;
+  return attn_plan((long long)B * H, T).slots_bytes * (backward ? 2 : 1);
+}
+
+int ttt_linear_attn_fwd(const void *Q, const void *K, const void *V, int qkv_dtype, const float *log_decay,
+                        const float *S0, const int *lengths, float scale, int B, int H, int T, int d, void *Z,
+                        float *S_out, void *workspace, size_t workspace_bytes, void *stream) {
+  return run_attn_fwd(Q, K, V, qkv_dtype, log_decay, S0, lengths, scale, B, H, T, d, Z, S_out, workspace,
+                      workspace_bytes, stream);
+}
+
+int ttt_linear_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype, const float *log_decay,
+                        const float *S0, const int *lengths, float scale, const void *dZ, const float *dS_T, int B,
+                        int H, int T, int d, void *dQ, void *dK, void *dV, float *dS0, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+  return run_attn_bwd(Q, K, V, qkv_dtype, log_decay, S0, lengths, scale, dZ, dS_T, B, H, T, d, dQ, dK, dV, dS0,
+                      workspace, workspace_bytes, stream);
+}
+
+int ttt_linear_attn_decode(const void *q, const void *k, const void *v, int qkv_dtype, const float *log_decay,
+                           float scale, float *S, const int *positions, const float *inv_freq, int rotary_dim,
+                           int interleaved, float mscale, int B, int H, int d, void *z, void *stream) {
+  return run_attn_decode(q, k, v, qkv_dtype, log_decay, scale, S, positions, inv_freq, rotary_dim, interleaved, mscale,
+                         B, H, d, z, stream);
+}
+
+int ttt_rope(const void *Q, const void *K, int dtype, const int *positions, int first_position, const float *inv_freq,
+             int rotary_dim, int interleaved, float mscale, int inverse, int B, int Hq, int Hk, int T, int d,
+             const long long *q_strides, const long long *k_strides, void *Q_out, void *K_out, void *stream) {
+  return run_rope(Q, K, dtype, positions, first_position, inv_freq, rotary_dim, interleaved, mscale, inverse, B, Hq, Hk,
+                  T, d, q_strides, k_strides, Q_out, K_out, stream);
 }
 
 }  // extern "C"

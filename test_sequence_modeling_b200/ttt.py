@@ -8,6 +8,9 @@ is no CPU path: tensors that are not on a CUDA device are rejected.
 """
 from __future__ import annotations
 
+import ctypes
+import math
+
 import torch
 
 from . import _lib
@@ -512,6 +515,252 @@ def _mlp_decode_args(q, k, v, eta, W1, W2, W1_base, W2_base, gamma, beta, z):
         _shaped(t, n, (H, d))
     z = _out(z, (B, H, d), q.device, "z")
     return _QKV_DTYPES[q.dtype], B, H, d, hidden, z
+
+
+class Rope:
+    """A rotary plan: inv_freq [rotary / 2] f32 (CUDA), the factor mscale on turned values, and
+    the layout of the pairs, (i, i + rotary / 2) or, interleaved, (2i, 2i + 1)."""
+
+    def __init__(self, inv_freq, mscale=1.0, interleaved=False):
+        _cuda(inv_freq, "inv_freq", torch.float32)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must have shape [rotary / 2]")
+        self.inv_freq = inv_freq
+        self.mscale = float(mscale)
+        self.interleaved = bool(interleaved)
+
+    @property
+    def rotary(self) -> int:
+        return 2 * self.inv_freq.numel()
+
+    @classmethod
+    def build(cls, rotary=64, base=10000.0, interleaved=False, scaling=None, factor=1.0, original_length=None,
+              beta_fast=32.0, beta_slow=1.0, device="cuda"):
+        """Frequencies base^(-2i / rotary), stretched for contexts `factor` times as long:
+        scaling "linear": every frequency divided by factor (positions interpolated);
+        "ntk": the base raised to base factor^(rotary / (rotary - 2)), which divides the
+        slowest frequency by factor and leaves the fastest;
+        "yarn": pairs that turn more than beta_fast times over original_length positions
+        keep their frequency, those that turn less than beta_slow times have it divided by
+        factor, a linear ramp over the pairs between; turned values get the factor
+        0.1 ln(factor) + 1."""
+        inv_freq, mscale = rope_frequencies(rotary, base, scaling, factor, original_length, beta_fast, beta_slow)
+        return cls(inv_freq.to(device), mscale, interleaved)
+
+
+def rope_frequencies(rotary, base=10000.0, scaling=None, factor=1.0, original_length=None, beta_fast=32.0,
+                     beta_slow=1.0):
+    """(inv_freq [rotary / 2] f32 on the host, mscale) of Rope.build."""
+    if rotary <= 0 or rotary % 2:
+        raise ValueError("rotary must be even and positive")
+    if not (base > 1.0 and math.isfinite(base)) or not (factor >= 1.0 and math.isfinite(factor)):
+        raise ValueError("base must be > 1 and factor >= 1")
+    i = torch.arange(rotary // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rotary == 2:
+            raise ValueError("scaling 'ntk' needs rotary > 2")
+        base = base * factor ** (rotary / (rotary - 2))
+    f = torch.pow(torch.tensor(base, dtype=torch.float64), -2.0 * i / rotary)
+    if scaling in (None, "ntk"):
+        return f.float(), 1.0
+    if scaling == "linear":
+        return (f / factor).float(), 1.0
+    if scaling == "yarn":
+        if not original_length or original_length <= 0 or not beta_fast > beta_slow > 0:
+            raise ValueError("scaling 'yarn' needs original_length > 0 and beta_fast > beta_slow > 0")
+
+        def pair_of(turns):  # the (fractional) pair that turns this often over original_length positions
+            return rotary * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        low = max(math.floor(pair_of(beta_fast)), 0)
+        high = min(math.ceil(pair_of(beta_slow)), rotary - 1)
+        slow = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+        return (f / factor * slow + f * (1.0 - slow)).float(), 0.1 * math.log(factor) + 1.0
+    raise ValueError(f"unknown scaling {scaling!r}: None, 'linear', 'ntk' or 'yarn'")
+
+
+def _ints(t, name, shape):
+    """An int32 CUDA tensor of exactly this shape."""
+    _cuda(t, name, torch.int32)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _same_device(Q, *tensors):
+    """The C ABI reads plain pointers of one device."""
+    for t in tensors:
+        if t is not None and t.device != Q.device:
+            raise ValueError(f"every tensor must be on {Q.device}, got {t.device}")
+
+
+def _out_as(t, like_shape, like, name):
+    if t is None:
+        return torch.empty(like_shape, dtype=like.dtype, device=like.device)
+    _cuda(t, name, like.dtype)
+    if tuple(t.shape) != tuple(like_shape):
+        raise ValueError(f"{name} must have shape {tuple(like_shape)}")
+    return t
+
+
+def _rope_rows(t, name):
+    """Checks a [B, H, T, d] tensor whose rows may lie at any strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
+    if t.dtype not in _QKV_DTYPES or t.dim() != 4:
+        raise TypeError(f"{name} must be a [B, H, T, d] tensor, float32 or bfloat16")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t
+
+
+def ttt_rope(Q, K, rope, positions=None, first_position=0, inverse=False, Q_out=None, K_out=None, stream=None):
+    """Rotary positions on Q [B,Hq,T,d] and K [B,Hk,T,d] (K may be None), f32 or bf16, at any
+    strides with contiguous rows (see include/ttt.h).  positions [B,T] int32, or None:
+    first_position + t.  inverse: the turn back, which is the forward's gradient.  Returns
+    (Q_out, K_out), dense [B,H,T,d] in the inputs' type (K_out None without K)."""
+    _rope_rows(Q, "Q")
+    B, Hq, T, d = Q.shape
+    Hk = 0
+    if K is not None:
+        _rope_rows(K, "K")
+        Hk = K.shape[1]
+        if K.dtype != Q.dtype or K.shape[0] != B or tuple(K.shape[2:]) != (T, d):
+            raise ValueError("K must have Q's type and shape but for the heads")
+        K_out = _out_as(K_out, (B, Hk, T, d), K, "K_out")
+    elif K_out is not None:
+        raise ValueError("K_out without K")
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    if positions is not None:
+        _ints(positions, "positions", (B, T))
+    Q_out = _out_as(Q_out, (B, Hq, T, d), Q, "Q_out")
+    _same_device(Q, K, rope.inv_freq, positions, Q_out, K_out)
+    strides = ctypes.c_longlong * 3
+    sq = strides(*Q.stride()[:3])
+    sk = strides(*K.stride()[:3]) if K is not None else None
+    with torch.cuda.device(Q.device):
+        st = _lib.load().ttt_rope(_ptr(Q), _ptr(K), _QKV_DTYPES[Q.dtype], _ptr(positions), int(first_position),
+                                  _ptr(rope.inv_freq), rope.rotary, int(rope.interleaved), rope.mscale,
+                                  int(bool(inverse)), B, Hq, Hk, T, d, sq, sk, _ptr(Q_out), _ptr(K_out),
+                                  _stream(stream, Q.device))
+    check(st, "ttt_rope")
+    return Q_out, K_out
+
+
+def linear_attn_workspace_bytes(shape, backward=False) -> int:
+    """Device workspace bytes of ttt_linear_attn_fwd (or _bwd) for inputs of `shape` [B,H,T,d]."""
+    B, H, T, d = shape
+    return int(_lib.load().ttt_linear_attn_workspace_bytes(B, H, T, d, int(bool(backward))))
+
+
+def _attn_args(Q, K, V, log_decay, scale, S0, lengths, workspace, backward):
+    dt = _qkv(Q, K, V)
+    B, H, T, d = Q.shape
+    _shaped(log_decay, "log_decay", (H,))
+    if S0 is not None:
+        _shaped(S0, "S0", (B, H, d, d))
+    if lengths is not None:
+        _ints(lengths, "lengths", (B,))
+    need = linear_attn_workspace_bytes((B, H, T, d), backward)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device) if need else None
+    else:
+        _cuda(workspace, "workspace", torch.uint8)
+    _same_device(Q, K, V, log_decay, S0, lengths, workspace)
+    return dt, (B, H, T, d), float(d ** -0.5 if scale is None else scale), workspace
+
+
+def _ws(workspace):
+    return (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
+
+
+def ttt_linear_attn_fwd(Q, K, V, log_decay, scale=None, S0=None, lengths=None, rope=None, positions=None, Z=None,
+                        S_out=None, workspace=None, stream=None):
+    """Linear attention with a decay for each head (see include/ttt.h): Q, K, V [B,H,T,d] (f32
+    or bf16), log_decay [H] f32, S0 [B,H,d,d] f32 or None, lengths [B] int32 or None (ends of
+    padded sequences), scale (default d^-1/2).  rope (a Rope; Q, K then at any strides): Q and
+    K are turned first, at positions [B,T] int32 or t.  workspace: a uint8 CUDA tensor of
+    linear_attn_workspace_bytes (allocated when None).  Returns (Z [B,H,T,d] in Q's type,
+    S_out [B,H,d,d] f32, the state to continue from or to decode with)."""
+    if rope is not None:
+        Q, K = ttt_rope(Q, K, rope, positions=positions, stream=stream)
+    elif positions is not None:
+        raise ValueError("positions without a rope")
+    dt, (B, H, T, d), scale, workspace = _attn_args(Q, K, V, log_decay, scale, S0, lengths, workspace, False)
+    Z = _out_as(Z, (B, H, T, d), Q, "Z")
+    S_out = _out(S_out, (B, H, d, d), Q.device, "S_out")
+    _same_device(Q, Z, S_out)
+    with torch.cuda.device(Q.device):
+        st = _lib.load().ttt_linear_attn_fwd(_ptr(Q), _ptr(K), _ptr(V), dt, _ptr(log_decay), _ptr(S0), _ptr(lengths),
+                                             scale, B, H, T, d, _ptr(Z), _ptr(S_out), *_ws(workspace),
+                                             _stream(stream, Q.device))
+    check(st, "ttt_linear_attn_fwd")
+    return Z, S_out
+
+
+def ttt_linear_attn_bwd(Q, K, V, log_decay, dZ, scale=None, S0=None, dS_T=None, lengths=None, rope=None,
+                        positions=None, workspace=None, stream=None):
+    """Backward of ttt_linear_attn_fwd on the same inputs: the gradients of <dZ, Z> + <dS_T,
+    S_out>.  dZ [B,H,T,d] in Q's type, dS_T [B,H,d,d] f32 or None.  Returns a dict: dQ, dK, dV
+    [B,H,T,d] in Q's type and dS0 [B,H,d,d] f32.  With a rope dQ and dK are those of the Q
+    and K before the turn."""
+    if rope is not None:
+        Q, K = ttt_rope(Q, K, rope, positions=positions, stream=stream)
+    elif positions is not None:
+        raise ValueError("positions without a rope")
+    dt, (B, H, T, d), scale, workspace = _attn_args(Q, K, V, log_decay, scale, S0, lengths, workspace, True)
+    _cuda(dZ, "dZ", Q.dtype)
+    if dZ.shape != Q.shape:
+        raise ValueError(f"dZ must have shape {tuple(Q.shape)}, got {tuple(dZ.shape)}")
+    if dS_T is not None:
+        _shaped(dS_T, "dS_T", (B, H, d, d))
+    _same_device(Q, dZ, dS_T)
+    out = {n: torch.empty_like(Q) for n in ("dQ", "dK", "dV")}
+    out["dS0"] = torch.empty(B, H, d, d, device=Q.device)
+    with torch.cuda.device(Q.device):
+        st = _lib.load().ttt_linear_attn_bwd(_ptr(Q), _ptr(K), _ptr(V), dt, _ptr(log_decay), _ptr(S0), _ptr(lengths),
+                                             scale, _ptr(dZ), _ptr(dS_T), B, H, T, d, _ptr(out["dQ"]),
+                                             _ptr(out["dK"]), _ptr(out["dV"]), _ptr(out["dS0"]), *_ws(workspace),
+                                             _stream(stream, Q.device))
+    check(st, "ttt_linear_attn_bwd")
+    if rope is not None:
+        out["dQ"], out["dK"] = ttt_rope(out["dQ"], out["dK"], rope, positions=positions, inverse=True, stream=stream)
+    return out
+
+
+def ttt_linear_attn_decode(q, k, v, log_decay, S, scale=None, rope=None, positions=None, z=None, stream=None):
+    """One token of ttt_linear_attn_fwd per (batch, head): q, k, v [B,H,d] (f32 or bf16),
+    log_decay [H] f32; the state S [B,H,d,d] f32 is updated in place.  rope (a Rope): q and k are
+    turned at positions [B] int32 in the same kernel.  Returns z [B,H,d] in q's type."""
+    for n, t in (("q", q), ("k", k), ("v", v)):
+        _cuda(t, n)
+    if not (q.dtype == k.dtype == v.dtype) or q.dtype not in _QKV_DTYPES:
+        raise TypeError("q, k, v must share one dtype, float32 or bfloat16")
+    if not (q.shape == k.shape == v.shape) or q.dim() != 3:
+        raise ValueError("q, k, v must have the same shape [B, H, d]")
+    B, H, d = q.shape
+    _shaped(log_decay, "log_decay", (H,))
+    _shaped(S, "S", (B, H, d, d))
+    if (rope is None) != (positions is None):
+        raise ValueError("rope and positions go together")
+    if rope is not None:
+        if not isinstance(rope, Rope):
+            raise TypeError("rope must be a Rope")
+        _ints(positions, "positions", (B,))
+    z = _out_as(z, (B, H, d), q, "z")
+    inv_freq = None if rope is None else rope.inv_freq
+    _same_device(q, k, v, log_decay, S, positions, inv_freq, z)
+    with torch.cuda.device(q.device):
+        st = _lib.load().ttt_linear_attn_decode(
+            _ptr(q), _ptr(k), _ptr(v), _QKV_DTYPES[q.dtype], _ptr(log_decay), float(d ** -0.5 if scale is None else scale),
+            _ptr(S), _ptr(positions), _ptr(inv_freq), 0 if rope is None else rope.rotary,
+            0 if rope is None else int(rope.interleaved), 1.0 if rope is None else rope.mscale, B, H, d, _ptr(z),
+            _stream(stream, q.device))
+    check(st, "ttt_linear_attn_decode")
+    return z
 
 
 def set_path(path: int) -> int:
