@@ -26,11 +26,13 @@
 #include "rope.cuh"
 #include "simt.cuh"
 #include "tc_linear.cuh"
+#include "tc_linear_attn.cuh"
 #include "tc_momentum.cuh"
 #include "tc_mlp.cuh"
 
 namespace simt = ttt::simt;
 namespace tc = ttt::tc;
+namespace tclattn = ttt::tclattn;
 namespace tcmlp = ttt::tcmlp;
 namespace decode = ttt::decode;
 namespace lattn = ttt::lattn;
@@ -770,8 +772,30 @@ int launch_attn(KernelT kernel, long long grid, int threads, size_t smem, cudaSt
   return TTT_OK;
 }
 
-// One pass of lattn::attn_kernel over all units.
+template <bool REVERSE, bool STATE_ONLY>
+int launch_attn_tc(long long units, const lattn::Params &p, cudaStream_t s) {
+  CUtensorMap mx, my, mw, mo;
+  if (!make_qkv_map(&my, p.Y, p.T, units, tclattn::CHUNK) || !make_qkv_map(&mw, p.W, p.T, units, tclattn::CHUNK) ||
+      !make_qkv_map(&mx, STATE_ONLY ? p.Y : p.X, p.T, units, tclattn::CHUNK) ||
+      !make_qkv_map(&mo, STATE_ONLY ? p.Y : p.out, p.T, units, tclattn::CHUNK))
+    return TTT_ERR_CUDA;
+  auto kernel = tclattn::attn_tc_kernel<REVERSE, STATE_ONLY>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tclattn::SMEM_BYTES) != cudaSuccess)
+    return TTT_ERR_CUDA;
+  kernel<<<(unsigned)(units * p.nseg), tclattn::THREADS, tclattn::SMEM_BYTES, s>>>(mx, my, mw, mo, p,
+                                                                                  g_inject_timeout.load());
+  if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return TTT_OK;
+}
+
+// One pass over all units: bf16 on the tensor cores (unless the CUDA-core path is selected),
+// everything else by lattn::attn_kernel.
 int attn_pass(bool bf16, bool reverse, long long units, const lattn::Params &p, cudaStream_t s) {
+  if (bf16 && p.T > 0 && g_path.load() != TTT_PATH_SIMT) {
+    if (!p.out) return reverse ? launch_attn_tc<true, true>(units, p, s) : launch_attn_tc<false, true>(units, p, s);
+    return reverse ? launch_attn_tc<true, false>(units, p, s) : launch_attn_tc<false, false>(units, p, s);
+  }
   const long long grid = units * p.nseg;
   auto kernel = bf16 ? (reverse ? lattn::attn_kernel<__nv_bfloat16, true> : lattn::attn_kernel<__nv_bfloat16, false>)
                      : (reverse ? lattn::attn_kernel<float, true> : lattn::attn_kernel<float, false>);
@@ -810,6 +834,7 @@ int run_attn_fwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
   const long long units = (long long)B * H;
   if (units == 0) return TTT_OK;
   const bool tok = T > 0, bf16 = qkv_dtype == TTT_BF16;
+  if (g_path.load() == TTT_PATH_TC && !bf16) return TTT_ERR_UNSUPPORTED;
   const size_t xb = (size_t)units * T * d * (bf16 ? 2 : 4), sb = (size_t)units * d * d * 4;
   const AttnPlan plan = attn_plan(units, T);
   if (plan.slots_bytes && (!workspace || workspace_bytes < plan.slots_bytes)) return TTT_ERR_ARG;
@@ -837,6 +862,7 @@ int run_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
   const long long units = (long long)B * H;
   if (units == 0) return TTT_OK;
   const bool tok = T > 0, bf16 = qkv_dtype == TTT_BF16;
+  if (g_path.load() == TTT_PATH_TC && !bf16) return TTT_ERR_UNSUPPORTED;
   const size_t xb = (size_t)units * T * d * (bf16 ? 2 : 4), sb = (size_t)units * d * d * 4;
   const AttnPlan plan = attn_plan(units, T);
   const size_t wb = 2 * plan.slots_bytes;
