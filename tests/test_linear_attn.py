@@ -247,6 +247,27 @@ def test_rope_and_attention_together(dtype):
     assert np.all(np.abs(z.double().cpu().numpy() - Zr[:, :, 0]) <= (130 * U32 * (A + 12) + U[dtype] * np.abs(Zr))[:, :, 0])
 
 
+@pytest.mark.parametrize("size", [(1, 32, 8192), (160, 1, 1000), (3, 7, 5000)], ids=str)
+@pytest.mark.parametrize("decay", ["slow", "slope"])
+def test_many_chunks_and_segments_on_both_paths(size, decay):
+    """bf16 on the tensor cores against the CUDA-core kernels in fp32 on the same values: U A for the
+    rounded operand and U |value| for the output (see bounds), with A from the same kernels on
+    absolute values, and each doubled for the reference's own roundings (far below them)."""
+    c = make(*size, "bf16", decay, True, back=True, seed=4)
+    x = device(c, "bf16")
+    exact = {n: (t.float() if isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 else t) for n, t in x.items()}
+    mags = {n: (t.abs() if isinstance(t, torch.Tensor) and n != "log_decay" else t) for n, t in exact.items()}
+    for run in (run_fwd, run_bwd):
+        for _ in range(3):
+            got = run(x)
+            want, mag = run(exact), run(mags)
+            for n, t in got.items():
+                u = 600 * U32 if n in ("S", "dS0") else U["bf16"] * (1 + 2.0 ** -6)
+                bound = u * mag[n] + (0 if n in ("S", "dS0") else U["bf16"] * (1 + 2.0 ** -6) * want[n].abs())
+                over = (t.float() - want[n]).abs() - bound
+                assert bool((over <= 1e-30).all()), (n, float(over.max()))
+
+
 # ---- calls a user makes that the sizes do not show ------------------------------------------
 
 def test_results_do_not_change_between_calls():
