@@ -782,8 +782,9 @@ int launch_attn_tc(long long units, const lattn::Params &p, cudaStream_t s) {
   auto kernel = tclattn::attn_tc_kernel<REVERSE, STATE_ONLY>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tclattn::SMEM_BYTES) != cudaSuccess)
     return TTT_ERR_CUDA;
-  kernel<<<(unsigned)(units * p.nseg), tclattn::THREADS, tclattn::SMEM_BYTES, s>>>(mx, my, mw, mo, p,
-                                                                                  g_inject_timeout.load());
+  const long long segments = units * p.nseg;
+  kernel<<<(unsigned)std::min<long long>(segments, ATTN_SMS), tclattn::THREADS, tclattn::SMEM_BYTES, s>>>(
+      mx, my, mw, mo, p, (int)segments, g_inject_timeout.load());
   if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return TTT_OK;
