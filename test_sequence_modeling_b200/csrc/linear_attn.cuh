@@ -43,21 +43,64 @@ constexpr int CHUNK = 64;
 constexpr int THREADS = 256;
 constexpr int LD = D + 4;  // padded row stride: 8 rows' float4 at one column hit 8 distinct bank groups
 
+// How the units' sequences are dealt out: units below `whole` are one segment each, the others are
+// cut into nseg segments of seg_len tokens (whole chunks of every kernel).  Segment k of the grid:
+struct Cut {
+  int whole, nseg, seg_len;
+  __host__ __device__ int segments(int units) const { return whole + (units - whole) * nseg; }
+};
+struct Segment {
+  int unit, seg;
+  int t_lo, rows;     // its rows (of T)
+  bool first, last;   // in the order of the pass
+  bool cut;           // it has a slot for the state it starts from ...
+  long long slot;     // ... this one
+};
+
 struct Params {
   const void *X, *Y, *W;   // [units][T][D]
   const float *log_decay;  // [H]
   const int *lengths;      // [B] or NULL
-  const float *C0;         // carried state at the start, or NULL (zero)
-  long long c0_stride;     // elements between units of C0 (a segment's slot follows its predecessor's)
-  bool c0_segments;        // C0 has a slot for each segment (else only the first one reads it)
-  bool c0_transposed;
+  const float *C0;         // [units][D][D] carried state at the start of the pass, or NULL (zero)
+  const float *slots;      // [cut units][nseg][D][D] states that the segments of cut units start from
+  bool transposed;         // the pass carries the transposes of C0 and of the slots
   float a, c, e;           // the three factors above
-  void *out;               // [units][T][D], or NULL: the state alone
-  float *C_out;            // carried state after the pass, or NULL
-  bool c_out_segments;     // C_out has a slot for each segment (else the last one writes it)
+  void *out;               // [units][T][D]
+  float *C_out;            // [units][D][D] carried state after the pass, or NULL
+  float *slots_out;        // [cut units][nseg][D][D], else NULL: no outputs, only the states that the cut
+                           // units' segments leave by themselves (the last one's has no reader)
   int H, T;
-  int seg_len, nseg;       // tokens a segment (a multiple of CHUNK), segments of a sequence
+  Cut cut;
+  int first_segment, segments;  // this launch's
 };
+
+template <bool REVERSE>
+__device__ __forceinline__ Segment segment_of(const Params &p, int k) {
+  Segment g;
+  const int rest = k - p.cut.whole;
+  g.cut = rest >= 0;
+  const int q = g.cut ? rest / p.cut.nseg : 0;
+  g.unit = g.cut ? p.cut.whole + q : k;
+  g.seg = g.cut ? rest - q * p.cut.nseg : 0;
+  const int n = g.cut ? p.cut.nseg : 1, len = g.cut ? p.cut.seg_len : p.T;
+  g.t_lo = g.seg * len;
+  g.rows = min(len, p.T - g.t_lo);
+  g.first = REVERSE ? g.seg == n - 1 : g.seg == 0;
+  g.last = REVERSE ? g.seg == 0 : g.seg == n - 1;
+  g.slot = g.cut ? (long long)rest * (D * D) : 0;
+  return g;
+}
+// The state a segment starts from (NULL: zero).
+__device__ __forceinline__ const float *start_state(const Params &p, const Segment &g) {
+  if (p.slots_out) return nullptr;
+  if (g.cut) return p.slots + g.slot;
+  return p.C0 ? p.C0 + (long long)g.unit * (D * D) : nullptr;
+}
+// Where the state it ends in goes (NULL: nowhere).
+__device__ __forceinline__ float *end_state(const Params &p, const Segment &g) {
+  if (p.slots_out) return g.last ? nullptr : p.slots_out + g.slot;
+  return p.C_out && g.last ? p.C_out + (long long)g.unit * (D * D) : nullptr;
+}
 
 __device__ __forceinline__ float decay_pow(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
 
@@ -95,33 +138,27 @@ __global__ void __launch_bounds__(THREADS) attn_kernel(const Params p) {
   float *Cs = Ms + CHUNK * LD;   // the carried state
   float *pw = Cs + D * LD;       // gamma^0 .. gamma^CHUNK
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const long long unit = blockIdx.x / p.nseg;
-  const int seg = blockIdx.x % p.nseg;
-  const int head = (int)(unit % p.H);
-  const bool first = REVERSE ? seg == p.nseg - 1 : seg == 0;
-  const bool last = REVERSE ? seg == 0 : seg == p.nseg - 1;
-  if (!p.out && p.c_out_segments && last) return;  // no segment follows it: its own state has no reader
-  const float g = p.log_decay[head];
-  const int len = sequence_length(p.lengths, (int)(unit / p.H), p.T);
-  const int t_lo = seg * p.seg_len;
-  const int t_hi = min(t_lo + p.seg_len, p.T);      // the segment's rows
-  const int n_seg = min(max(len - t_lo, 0), t_hi - t_lo);  // its tokens
-  const long long row0 = unit * p.T + t_lo;
+  const Segment sg = segment_of<REVERSE>(p, p.first_segment + blockIdx.x);
+  const bool state_only = p.slots_out != nullptr;
+  if (state_only && sg.last) return;
+  const float g = p.log_decay[sg.unit % p.H];
+  const int len = sequence_length(p.lengths, sg.unit / p.H, p.T);
+  const int n_seg = min(max(len - sg.t_lo, 0), sg.rows);  // its tokens
+  const long long row0 = (long long)sg.unit * p.T + sg.t_lo;
   const InT *X = static_cast<const InT *>(p.X) + row0 * D;
   const InT *Y = static_cast<const InT *>(p.Y) + row0 * D;
   const InT *W = static_cast<const InT *>(p.W) + row0 * D;
-  InT *out = p.out ? static_cast<InT *>(p.out) + row0 * D : nullptr;
+  InT *out = state_only ? nullptr : static_cast<InT *>(p.out) + row0 * D;
 
   // The state at the start of the pass: this thread's rows ty + 16 i, columns 4 tx .. 4 tx + 3.
-  const float *C0 = nullptr;
-  if (p.C0 && (p.c0_segments || first)) C0 = p.C0 + unit * p.c0_stride + (p.c0_segments ? (long long)seg * D * D : 0);
+  const float *C0 = start_state(p, sg);
   float C[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = ty + 16 * i, col = 4 * tx + j;
-      C[i][j] = C0 ? (p.c0_transposed ? C0[col * D + r] : C0[r * D + col]) : 0.f;
+      C[i][j] = C0 ? (p.transposed ? C0[col * D + r] : C0[r * D + col]) : 0.f;
       Cs[r * LD + col] = C[i][j];
     }
   }
@@ -246,49 +283,59 @@ __global__ void __launch_bounds__(THREADS) attn_kernel(const Params p) {
   }
   // Rows behind the end.
   if (out) {
-    const int rows = t_hi - t_lo;
-    for (int r = n_seg + ty; r < rows; r += 16) store_out(out + (long long)r * D + 4 * tx, make_float4(0.f, 0.f, 0.f, 0.f));
+    for (int r = n_seg + ty; r < sg.rows; r += 16) store_out(out + (long long)r * D + 4 * tx, make_float4(0.f, 0.f, 0.f, 0.f));
   }
-  if (p.C_out && (p.c_out_segments || last)) {
-    float *Co = p.C_out + (p.c_out_segments ? (unit * p.nseg + seg) : unit) * (long long)(D * D);
+  if (float *Co = end_state(p, sg)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<float4 *>(Co + (ty + 16 * i) * D + 4 * tx) = make_float4(C[i][0], C[i][1], C[i][2], C[i][3]);
   }
 }
 
-// The states at the segments' starts, in place: slot i of a unit holds the state that its
-// segment alone leaves (M_i) and gets the state that it starts from,
+// The states at the segments' starts of the cut units, in place: slot i of a unit holds the state that
+// its segment alone leaves (M_i) and gets the state that it starts from,
 //   C_0 = C0,  C_{i+1} = gamma^(n_i) C_i + M_i     (reverse: from the last segment down).
 // Reads and writes nseg x 16 KB a unit once: bound by memory, and small beside the tokens.
 struct ScanParams {
-  float *slots;  // [units][nseg][D][D]
+  float *slots;  // [cut units][nseg][D][D]
   const float *C0;
   const float *log_decay;
   const int *lengths;
-  int H, T, seg_len, nseg;
+  int H, T;
+  Cut cut;
 };
 
 constexpr int SCAN_THREADS = 256;  // 4 values a thread: 4 CTAs a unit
 
 template <bool REVERSE>
 __global__ void __launch_bounds__(SCAN_THREADS) scan_kernel(const ScanParams p) {
-  const long long unit = blockIdx.x >> 2;
+  const int q = blockIdx.x >> 2, unit = p.cut.whole + q;
   const int at = ((blockIdx.x & 3) * SCAN_THREADS + threadIdx.x) * 4;
   const float g = p.log_decay[unit % p.H];
-  const int len = sequence_length(p.lengths, (int)(unit / p.H), p.T);
+  const int len = sequence_length(p.lengths, unit / p.H, p.T);
   float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.C0) c = *reinterpret_cast<const float4 *>(p.C0 + unit * (long long)(D * D) + at);
-  float *slots = p.slots + unit * p.nseg * (long long)(D * D) + at;
-  for (int k = 0; k < p.nseg; ++k) {
-    const int i = REVERSE ? p.nseg - 1 - k : k;
-    float4 *slot = reinterpret_cast<float4 *>(slots + (long long)i * D * D);
-    const bool more = k + 1 < p.nseg;  // the last segment's own state has no reader
-    const float4 m = more ? *slot : c;
-    *slot = c;
-    const int t_lo = i * p.seg_len;
-    const float dn = decay_pow(g, min(max(len - t_lo, 0), min(p.seg_len, p.T - t_lo)));
-    c = make_float4(fmaf(dn, c.x, m.x), fmaf(dn, c.y, m.y), fmaf(dn, c.z, m.z), fmaf(dn, c.w, m.w));
+  if (p.C0) c = *reinterpret_cast<const float4 *>(p.C0 + (long long)unit * (D * D) + at);
+  float *slots = p.slots + (long long)q * p.cut.nseg * (D * D) + at;
+  auto slot = [&](int k) {
+    return reinterpret_cast<float4 *>(slots + (long long)(REVERSE ? p.cut.nseg - 1 - k : k) * (D * D));
+  };
+  // In batches, whose loads do not wait for one another.
+  constexpr int BATCH = 8;
+  for (int k0 = 0; k0 < p.cut.nseg; k0 += BATCH) {
+    float4 m[BATCH];
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j)
+      if (k0 + j + 1 < p.cut.nseg) m[j] = *slot(k0 + j);
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const int k = k0 + j;
+      if (k < p.cut.nseg) *slot(k) = c;
+      if (k + 1 < p.cut.nseg) {
+        const int t_lo = (REVERSE ? p.cut.nseg - 1 - k : k) * p.cut.seg_len;
+        const float dn = decay_pow(g, min(max(len - t_lo, 0), min(p.cut.seg_len, p.T - t_lo)));
+        c = make_float4(fmaf(dn, c.x, m[j].x), fmaf(dn, c.y, m[j].y), fmaf(dn, c.z, m[j].z), fmaf(dn, c.w, m[j].w));
+      }
+    }
   }
 }
 

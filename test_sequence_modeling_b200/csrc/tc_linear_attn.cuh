@@ -128,6 +128,16 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, wait(bar, parity, abort));
 }
 
+// x less a pair of bf16 numbers, exact for the numbers nearest to x.
+__device__ __forceinline__ float2 minus_bf16x2(float2 x, uint32_t b) {
+  float2 d;
+  asm("{\n\t.reg .b16 lo, hi, m;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
+      "fma.rn.f32.bf16 %0, lo, m, %3;\n\tfma.rn.f32.bf16 %1, hi, m, %4;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "r"(b), "f"(x.x), "f"(x.y));
+  return d;
+}
+
 // After tmem_wait_ld: registers that a tensor memory load filled, not to be used before this place.
 template <int N>
 __device__ __forceinline__ void loaded(uint32_t (&r)[N]) {
@@ -147,7 +157,7 @@ template <bool REVERSE, bool STATE_ONLY>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY,
                    const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmOut, const Params p,
-                   const int nsegments, const int inject_timeout) {
+                   const int inject_timeout) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(sm);
@@ -181,19 +191,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after_sync();
   const uint32_t tb = *tslot;  // all columns are this CTA's: the base is 0, which the roles take as a constant
 
-  // Segment k of the grid: its unit and place, its rows and tokens.
-  struct Segment {
-    int unit, seg, t_lo, rows, n, nchunks;
-    bool first, last;
+  // This CTA's segments, their tokens and chunks.
+  const int k0 = p.first_segment + blockIdx.x, k1 = p.first_segment + p.segments;
+  struct Segment : lattn::Segment {
+    int n, nchunks;
   };
   auto segment = [&](int k) {
     Segment g;
-    g.unit = k / p.nseg;
-    g.seg = k - g.unit * p.nseg;
-    g.t_lo = g.seg * p.seg_len;
-    g.rows = min(p.seg_len, p.T - g.t_lo);
-    g.first = REVERSE ? g.seg == p.nseg - 1 : g.seg == 0;
-    g.last = REVERSE ? g.seg == 0 : g.seg == p.nseg - 1;
+    static_cast<lattn::Segment &>(g) = lattn::segment_of<REVERSE>(p, k);
     g.n = min(max(lattn::sequence_length(p.lengths, g.unit / p.H, p.T) - g.t_lo, 0), g.rows);
     if (STATE_ONLY && g.last) g.n = 0;  // no segment follows it: its own state has no reader
     g.nchunks = (g.n + CHUNK - 1) / CHUNK;
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---- loads -------------------------------------------------------------------
     if (lane == 0) {
       int i = 0;
-      for (int k = blockIdx.x; ok && k < nsegments; k += gridDim.x) {
+      for (int k = k0; ok && k < k1; k += gridDim.x) {
         const Segment g = segment(k);
         for (int c = 0; ok && c < g.nchunks; ++c, ++i) {
           const int slot = i & 1, t0 = g.t_lo + chunk_start(g, c);
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr uint32_t ID_PW = idesc_bf16_f32(128, 64, false, true, false);
     constexpr uint32_t ID_M = idesc_bf16_f32(64, 192, true, true, false);
     int total = 0;
-    for (int k = blockIdx.x; k < nsegments; k += gridDim.x) total += segment(k).nchunks;
+    for (int k = k0; k < k1; k += gridDim.x) total += segment(k).nchunks;
     auto scores = [&](int i) {  // P of chunk i, once its tiles are in
       const uint32_t slot = i & 1, par = (uint32_t)(i >> 1) & 1u;
       if (!wait_warp(&bars[FX + slot], par, abort) || !wait_warp(&bars[FY + slot], par, abort)) return false;
@@ -304,7 +309,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int half = (warp - 4) >> 2, ptid = tid - 128;
     const uint32_t row = tmem_addr(0, 32 * w4, T_P), dst = tmem_addr(0, 32 * w4, T_PB);
     int i = 0;
-    for (int k = blockIdx.x; k < nsegments; k += gridDim.x) {
+    for (int k = k0; k < k1; k += gridDim.x) {
       const Segment g = segment(k);
       if (g.nchunks == 0) continue;
       const float ld = log_decay(g);
@@ -376,35 +381,35 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int s = 32 * w4 + lane;
     const uint32_t row = sw128_offset(s, 0);  // piece q of the row is at row ^ (16 q)
     int i = 0;
-    for (int k = blockIdx.x; ok && k < nsegments; k += gridDim.x) {
+    for (int k = k0; ok && k < k1; k += gridDim.x) {
       const Segment g = segment(k);
       const float ld = log_decay(g);
       const float h_full = p.e * decay_pow(ld, REVERSE ? s + 1 : CHUNK - 1 - s);
       for (int c = 0; ok && c < g.nchunks; ++c, ++i) {
         const int n = min(CHUNK, g.n - chunk_start(g, c));
         const uint32_t slot = i & 1, par2 = (uint32_t)(i >> 1) & 1u;
-        const uint8_t *ty = sm + OFF_Y + slot * TILE;
+        uint8_t *ty = sm + OFF_Y + slot * TILE;
         uint8_t *ys = sm + OFF_YS + slot * (3 * TILE);
+        if (!(ok = wait_warp(&bars[FY + slot], par2, abort))) break;
+        // The buffer is free when the product that read it, two chunks ago, is done.
+        if (i > 1 && !(ok = wait_warp(&bars[MFULL + slot], par2 ^ 1u, abort))) break;
         float h1 = h_full;
         if (n < CHUNK) {
           if (!REVERSE) h1 = p.e * decay_pow(ld, max(n - 1 - s, 0));
           if (!(ok = wait_warp(&bars[FW + slot], par2, abort))) break;
           if (s >= n) {
-            h1 = 0.f;
 #pragma unroll 1
-            for (uint32_t q = 0; q < 128; q += 16)
+            for (uint32_t q = 0; q < 128; q += 16) {
+              *reinterpret_cast<uint4 *>(ty + (row ^ q)) = make_uint4(0u, 0u, 0u, 0u);
               *reinterpret_cast<uint4 *>(sm + OFF_W + slot * TILE + (row ^ q)) = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
         }
         const float2 h = make_float2(h1, h1);
-        if (!(ok = wait_warp(&bars[FY + slot], par2, abort))) break;
-        // The buffer is free when the product that read it, two chunks ago, is done.
-        if (i > 1 && !(ok = wait_warp(&bars[MFULL + slot], par2 ^ 1u, abort))) break;
         uint4 y = *reinterpret_cast<const uint4 *>(ty + row);
 #pragma unroll 1
         for (uint32_t q = 0; q < 128; q += 16) {
-          uint32_t u[4] = {y.x, y.y, y.z, y.w};
-          if (s >= n) u[0] = u[1] = u[2] = u[3] = 0u;
+          const uint32_t u[4] = {y.x, y.y, y.z, y.w};
           y = *reinterpret_cast<const uint4 *>(ty + (row ^ ((q + 16) & 127)));
           uint32_t part[3][4];
 #pragma unroll
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int m = 0; m < 3; ++m) {
               part[m][e] = pack_bf16x2(r.x, r.y);
-              if (m < 2) r = __ffma2_rn(unpack_bf16x2(part[m][e]), make_float2(-1.f, -1.f), r);
+              if (m < 2) r = minus_bf16x2(r, part[m][e]);
             }
           }
 #pragma unroll
@@ -436,19 +441,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     // C[4 j + {2, 3}].
     const int row = 16 * w4 + (lane >> 2), col = 2 * (lane & 3);
     int i = 0;
-    for (int k = blockIdx.x; ok && k < nsegments; k += gridDim.x) {
+    for (int k = k0; ok && k < k1; k += gridDim.x) {
       const Segment g = segment(k);
       const float ld = log_decay(g);
       const float d_full = decay_pow(ld, CHUNK);
       float C[32];
       {
-        const float *C0 = nullptr;
-        if (p.C0 && (p.c0_segments || g.first))
-          C0 = p.C0 + (long long)g.unit * p.c0_stride + (p.c0_segments ? (long long)g.seg * D * D : 0);
+        const float *C0 = lattn::start_state(p, g);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int r = row + 8 * ((e >> 1) & 1), cc = 8 * (e >> 2) + col + (e & 1);
-          C[e] = C0 ? (p.c0_transposed ? C0[r * D + cc] : C0[cc * D + r]) : 0.f;
+          C[e] = C0 ? (p.transposed ? C0[r * D + cc] : C0[cc * D + r]) : 0.f;
         }
       }
       for (int c = 0; c < g.nchunks; ++c, ++i) {
@@ -487,8 +490,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      if (p.C_out && (p.c_out_segments ? !g.last : g.last)) {
-        float *Co = p.C_out + (p.c_out_segments ? ((long long)g.unit * p.nseg + g.seg) : g.unit) * (long long)(D * D);
+      if (float *Co = lattn::end_state(p, g)) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) Co[(8 * (e >> 2) + col + (e & 1)) * D + row + 8 * ((e >> 1) & 1)] = C[e];
       }
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---- outputs --------------------------------------------------------------------
     const int t = 32 * w4 + lane;
     int i = 0;
-    for (int k = blockIdx.x; k < nsegments; k += gridDim.x) {
+    for (int k = k0; k < k1; k += gridDim.x) {
       const Segment g = segment(k);
       const float ld = log_decay(g);
       const float f_full = p.c * decay_pow(ld, REVERSE ? CHUNK - 1 - t : t + 1);

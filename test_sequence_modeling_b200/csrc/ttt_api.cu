@@ -739,26 +739,44 @@ int check_buffers(std::initializer_list<Buffer> ins, std::initializer_list<Buffe
   return TTT_OK;
 }
 
-// How a sequence is cut.  With units (batch x heads) enough for every SM each one runs its
-// sequence alone; with fewer, the sequences are cut into segments of whole chunks that run side
-// by side, which costs a pass over half of the inputs for the segments' own states.
+// How the units (batch x heads) are dealt out to the SMs, one segment an SM at a time.  Whole units
+// fill rounds of all SMs; those that would be left for a last, unfilled round (or all of them where
+// there are fewer units than SMs) may be cut into segments that fill it, which costs a pass over half
+// of their inputs for the segments' own states.  The cut with the least time is taken, in steps of
+// one chunk on one SM: `passes` passes of ceil(segments / SMs) rounds each and as many state passes as
+// the call needs, a step of which takes ATTN_STATE_STEP of a full one, ATTN_SEGMENT_STEPS for each
+// segment's start and end, and ATTN_CUT_STEPS for the two more launches of a state pass.  Measured on one B200 (forward, bf16): B16 H12 T2048, 44 of 192 units
+// cut in three, against none cut; B1 H32 T32768 cut in nine, against four (see the kernel's table).
 struct AttnPlan {
-  int seg_len, nseg;
+  lattn::Cut cut;
   size_t slots_bytes;  // one set of segment states
 };
 constexpr int ATTN_SMS = 148;          // SMs of a B200: the workspace size does not ask a device
-constexpr int ATTN_SEG_ALIGN = 128;    // tokens: whole chunks of every kernel
-constexpr int ATTN_SEG_MIN = 512;      // tokens a segment at least
-AttnPlan attn_plan(long long units, int T) {
-  AttnPlan a{T > 0 ? T : 1, 1, 0};
-  if (units >= ATTN_SMS || units == 0 || T <= ATTN_SEG_MIN) return a;
-  const long long want = std::min<long long>(2 * ATTN_SMS / units, (T + ATTN_SEG_MIN - 1) / ATTN_SEG_MIN);
-  if (want < 2) return a;
-  const long long len = (T + want - 1) / want;
-  a.seg_len = (int)((len + ATTN_SEG_ALIGN - 1) / ATTN_SEG_ALIGN * ATTN_SEG_ALIGN);
-  a.nseg = (T + a.seg_len - 1) / a.seg_len;
-  a.slots_bytes = a.nseg > 1 ? (size_t)units * a.nseg * lattn::D * lattn::D * 4 : 0;
-  return a;
+constexpr int ATTN_CHUNK = 128;        // tokens of a step
+constexpr int ATTN_MOST_SEGMENTS = 64;
+constexpr double ATTN_STATE_STEP = 0.55;
+constexpr double ATTN_SEGMENT_STEPS = 0.7;
+constexpr double ATTN_CUT_STEPS = 4;
+AttnPlan attn_plan(long long units, int T, bool backward) {
+  AttnPlan best{{(int)units, 1, T > 0 ? T : 1}, 0};
+  const long long left = units % ATTN_SMS, chunks = ((long long)T + ATTN_CHUNK - 1) / ATTN_CHUNK;
+  if (left == 0 || chunks < 2) return best;
+  const int passes = backward ? 3 : 1, states = backward ? 2 : 1;
+  auto rounds = [](long long n) { return (double)((n + ATTN_SMS - 1) / ATTN_SMS); };
+  double least = passes * (chunks + ATTN_SEGMENT_STEPS);
+  for (int n = 2; n <= ATTN_MOST_SEGMENTS && n <= chunks; ++n) {
+    const long long len = (chunks + n - 1) / n, nseg = (chunks + len - 1) / len;
+    if (nseg != n) continue;
+    const double cost =
+        passes * rounds(left * n) * (len + ATTN_SEGMENT_STEPS) +
+        states * (rounds(left * (n - 1)) * (len * ATTN_STATE_STEP + ATTN_SEGMENT_STEPS) + ATTN_CUT_STEPS);
+    if (cost < least) {
+      least = cost;
+      best.cut = {(int)(units - left), n, (int)(len * ATTN_CHUNK)};
+      best.slots_bytes = (size_t)left * n * lattn::D * lattn::D * 4;
+    }
+  }
+  return best;
 }
 
 template <typename KernelT, typename ParamsT>
@@ -782,38 +800,39 @@ int launch_attn_tc(long long units, const lattn::Params &p, cudaStream_t s) {
   auto kernel = tclattn::attn_tc_kernel<REVERSE, STATE_ONLY>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tclattn::SMEM_BYTES) != cudaSuccess)
     return TTT_ERR_CUDA;
-  const long long segments = units * p.nseg;
-  kernel<<<(unsigned)std::min<long long>(segments, ATTN_SMS), tclattn::THREADS, tclattn::SMEM_BYTES, s>>>(
-      mx, my, mw, mo, p, (int)segments, g_inject_timeout.load());
+  kernel<<<(unsigned)std::min(p.segments, ATTN_SMS), tclattn::THREADS, tclattn::SMEM_BYTES, s>>>(
+      mx, my, mw, mo, p, g_inject_timeout.load());
   if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return TTT_OK;
 }
 
-// One pass over all units: bf16 on the tensor cores (unless the CUDA-core path is selected),
-// everything else by lattn::attn_kernel.
-int attn_pass(bool bf16, bool reverse, long long units, const lattn::Params &p, cudaStream_t s) {
+// One pass over all units (or, without an output, over the cut ones): bf16 on the tensor cores (unless
+// the CUDA-core path is selected), everything else by lattn::attn_kernel.
+int attn_pass(bool bf16, bool reverse, long long units, lattn::Params p, cudaStream_t s) {
+  const bool state_only = p.slots_out != nullptr;
+  p.first_segment = state_only ? p.cut.whole : 0;
+  p.segments = p.cut.segments((int)units) - p.first_segment;
   if (bf16 && p.T > 0 && g_path.load() != TTT_PATH_SIMT) {
-    if (!p.out) return reverse ? launch_attn_tc<true, true>(units, p, s) : launch_attn_tc<false, true>(units, p, s);
+    if (state_only) return reverse ? launch_attn_tc<true, true>(units, p, s) : launch_attn_tc<false, true>(units, p, s);
     return reverse ? launch_attn_tc<true, false>(units, p, s) : launch_attn_tc<false, false>(units, p, s);
   }
-  const long long grid = units * p.nseg;
   auto kernel = bf16 ? (reverse ? lattn::attn_kernel<__nv_bfloat16, true> : lattn::attn_kernel<__nv_bfloat16, false>)
                      : (reverse ? lattn::attn_kernel<float, true> : lattn::attn_kernel<float, false>);
-  return launch_attn(kernel, grid, lattn::THREADS, lattn::SMEM_BYTES, s, p);
+  return launch_attn(kernel, p.segments, lattn::THREADS, lattn::SMEM_BYTES, s, p);
 }
 
-// The states that the segments start from, into `slots`: the segments' own states, then the scan.
+// The states that the cut units' segments start from, into `slots`: the segments' own states, then the scan.
 int attn_segment_states(bool bf16, bool reverse, long long units, const AttnPlan &plan, const void *Y, const void *W,
                         float e, const float *log_decay, const int *lengths, const float *C0, int H, int T,
                         float *slots, cudaStream_t s) {
-  lattn::Params p{Y, Y, W, log_decay, lengths, nullptr, 0, false, false, 0.f, 0.f, e, nullptr, slots, true,
-                  H, T, plan.seg_len, plan.nseg};
+  lattn::Params p{Y, Y, W, log_decay, lengths, nullptr, nullptr, false, 0.f, 0.f, e, nullptr, nullptr, slots, H, T,
+                  plan.cut, 0, 0};
   int st = attn_pass(bf16, reverse, units, p, s);
   if (st != TTT_OK) return st;
-  lattn::ScanParams sp{slots, C0, log_decay, lengths, H, T, plan.seg_len, plan.nseg};
-  return launch_attn(reverse ? lattn::scan_kernel<true> : lattn::scan_kernel<false>, units * 4, lattn::SCAN_THREADS, 0,
-                     s, sp);
+  lattn::ScanParams sp{slots, C0, log_decay, lengths, H, T, plan.cut};
+  return launch_attn(reverse ? lattn::scan_kernel<true> : lattn::scan_kernel<false>, (units - plan.cut.whole) * 4,
+                     lattn::SCAN_THREADS, 0, s, sp);
 }
 
 // Sizes shared by the linear attention entry points over sequences.
@@ -837,7 +856,7 @@ int run_attn_fwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
   const bool tok = T > 0, bf16 = qkv_dtype == TTT_BF16;
   if (g_path.load() == TTT_PATH_TC && !bf16) return TTT_ERR_UNSUPPORTED;
   const size_t xb = (size_t)units * T * d * (bf16 ? 2 : 4), sb = (size_t)units * d * d * 4;
-  const AttnPlan plan = attn_plan(units, T);
+  const AttnPlan plan = attn_plan(units, T, false);
   if (plan.slots_bytes && (!workspace || workspace_bytes < plan.slots_bytes)) return TTT_ERR_ARG;
   st = check_buffers({{Q, xb, tok}, {K, xb, tok}, {V, xb, tok}, {log_decay, (size_t)H * 4, true}, {S0, sb, false},
                       {lengths, (size_t)B * 4, false}},
@@ -845,13 +864,12 @@ int run_attn_fwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
   if (st != TTT_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float *slots = static_cast<float *>(workspace);
-  const bool cut = plan.nseg > 1;
-  if (cut) {
+  if (plan.slots_bytes) {
     st = attn_segment_states(bf16, false, units, plan, K, V, 1.f, log_decay, lengths, S0, H, T, slots, s);
     if (st != TTT_OK) return st;
   }
-  lattn::Params p{Q, K, V, log_decay, lengths, cut ? slots : S0, (long long)(cut ? plan.nseg : 1) * d * d, cut, false,
-                  scale, scale, 1.f, Z, S_out, false, H, T, plan.seg_len, plan.nseg};
+  lattn::Params p{Q, K, V, log_decay, lengths, S0, slots, false, scale, scale, 1.f, Z, S_out, nullptr, H, T,
+                  plan.cut, 0, 0};
   return attn_pass(bf16, false, units, p, s);
 }
 
@@ -865,7 +883,7 @@ int run_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
   const bool tok = T > 0, bf16 = qkv_dtype == TTT_BF16;
   if (g_path.load() == TTT_PATH_TC && !bf16) return TTT_ERR_UNSUPPORTED;
   const size_t xb = (size_t)units * T * d * (bf16 ? 2 : 4), sb = (size_t)units * d * d * 4;
-  const AttnPlan plan = attn_plan(units, T);
+  const AttnPlan plan = attn_plan(units, T, true);
   const size_t wb = 2 * plan.slots_bytes;
   if (wb && (!workspace || workspace_bytes < wb)) return TTT_ERR_ARG;
   st = check_buffers({{Q, xb, tok}, {K, xb, tok}, {V, xb, tok}, {dZ, xb, tok}, {log_decay, (size_t)H * 4, true},
@@ -873,23 +891,20 @@ int run_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
                      {{dQ, xb, tok}, {dK, xb, tok}, {dV, xb, tok}, {dS0, sb, false}, {wb ? workspace : nullptr, wb, false}});
   if (st != TTT_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  float *slots_s = static_cast<float *>(workspace), *slots_g = slots_s;
-  const bool cut = plan.nseg > 1;
-  if (cut) {
+  float *slots_s = static_cast<float *>(workspace), *slots_g = nullptr;
+  if (plan.slots_bytes) {
     slots_g = slots_s + plan.slots_bytes / 4;
     st = attn_segment_states(bf16, false, units, plan, K, V, 1.f, log_decay, lengths, S0, H, T, slots_s, s);
     if (st != TTT_OK) return st;
     st = attn_segment_states(bf16, true, units, plan, Q, dZ, scale, log_decay, lengths, dS_T, H, T, slots_g, s);
     if (st != TTT_OK) return st;
   }
-  const float *Cs = cut ? slots_s : S0, *Cg = cut ? slots_g : dS_T;
-  const long long stride = (long long)(cut ? plan.nseg : 1) * d * d;
-  lattn::Params pq{dZ, V, K, log_decay, lengths, Cs, stride, cut, true, scale, scale, 1.f, dQ, nullptr, false,
-                   H, T, plan.seg_len, plan.nseg};
-  lattn::Params pk{V, dZ, Q, log_decay, lengths, Cg, stride, cut, true, scale, 1.f, scale, dK, nullptr, false,
-                   H, T, plan.seg_len, plan.nseg};
-  lattn::Params pv{K, Q, dZ, log_decay, lengths, Cg, stride, cut, false, scale, 1.f, scale, dV, dS0, false,
-                   H, T, plan.seg_len, plan.nseg};
+  lattn::Params pq{dZ, V, K, log_decay, lengths, S0, slots_s, true, scale, scale, 1.f, dQ, nullptr, nullptr, H, T,
+                   plan.cut, 0, 0};
+  lattn::Params pk{V, dZ, Q, log_decay, lengths, dS_T, slots_g, true, scale, 1.f, scale, dK, nullptr, nullptr, H, T,
+                   plan.cut, 0, 0};
+  lattn::Params pv{K, Q, dZ, log_decay, lengths, dS_T, slots_g, false, scale, 1.f, scale, dV, dS0, nullptr, H, T,
+                   plan.cut, 0, 0};
   if (tok) {
     if ((st = attn_pass(bf16, false, units, pq, s)) != TTT_OK) return st;
     if ((st = attn_pass(bf16, true, units, pk, s)) != TTT_OK) return st;
@@ -1370,7 +1385,7 @@ int ttt_linear_ln_decode(const void *q, const void *k, const void *v, int qkv_dt
 
 size_t ttt_linear_attn_workspace_bytes(int B, int H, int T, int d, int backward) {
   if (B < 0 || H < 0 || T < 0 || check_attn_sizes(TTT_F32, 1.f, B, H, T, d) != TTT_OK) return 0;
-  return attn_plan((long long)B * H, T).slots_bytes * (backward ? 2 : 1);
+  return attn_plan((long long)B * H, T, backward != 0).slots_bytes * (backward ? 2 : 1);
 }
 
 int ttt_linear_attn_fwd(const void *Q, const void *K, const void *V, int qkv_dtype, const float *log_decay,
