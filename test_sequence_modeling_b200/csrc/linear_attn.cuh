@@ -43,18 +43,17 @@ constexpr int CHUNK = 64;
 constexpr int THREADS = 256;
 constexpr int LD = D + 4;  // padded row stride: 8 rows' float4 at one column hit 8 distinct bank groups
 
-// How the units' sequences are dealt out: units below `whole` are one segment each, the others are
+// How the units' sequences are dealt out to segments: units below `whole` are one segment each, the others are
 // cut into nseg segments of seg_len tokens (whole chunks of every kernel).  Segment k of the grid:
 struct Cut {
   int whole, nseg, seg_len;
   __host__ __device__ int segments(int units) const { return whole + (units - whole) * nseg; }
 };
 struct Segment {
-  int unit, seg;
+  int unit;
   int t_lo, rows;     // its rows (of T)
-  bool first, last;   // in the order of the pass
-  bool cut;           // it has a slot for the state it starts from ...
-  long long slot;     // ... this one
+  bool last;          // of its unit, in the order of the pass
+  int slot;           // of the state that it starts from, or -1: it is its unit's first
 };
 
 struct Params {
@@ -62,7 +61,7 @@ struct Params {
   const float *log_decay;  // [H]
   const int *lengths;      // [B] or NULL
   const float *C0;         // [units][D][D] carried state at the start of the pass, or NULL (zero)
-  const float *slots;      // [cut units][nseg][D][D] states that the segments of cut units start from
+  float *slots;            // [cut units][nseg][D][D] states that the segments of cut units start from
   bool transposed;         // the pass carries the transposes of C0 and of the slots
   float a, c, e;           // the three factors above
   void *out;               // [units][T][D]
@@ -78,27 +77,25 @@ template <bool REVERSE>
 __device__ __forceinline__ Segment segment_of(const Params &p, int k) {
   Segment g;
   const int rest = k - p.cut.whole;
-  g.cut = rest >= 0;
-  const int q = g.cut ? rest / p.cut.nseg : 0;
-  g.unit = g.cut ? p.cut.whole + q : k;
-  g.seg = g.cut ? rest - q * p.cut.nseg : 0;
-  const int n = g.cut ? p.cut.nseg : 1, len = g.cut ? p.cut.seg_len : p.T;
-  g.t_lo = g.seg * len;
+  const bool cut = rest >= 0;
+  const int q = cut ? rest / p.cut.nseg : 0, seg = cut ? rest - q * p.cut.nseg : 0;
+  const int n = cut ? p.cut.nseg : 1, len = cut ? p.cut.seg_len : p.T;
+  g.unit = cut ? p.cut.whole + q : k;
+  g.t_lo = seg * len;
   g.rows = min(len, p.T - g.t_lo);
-  g.first = REVERSE ? g.seg == n - 1 : g.seg == 0;
-  g.last = REVERSE ? g.seg == 0 : g.seg == n - 1;
-  g.slot = g.cut ? (long long)rest * (D * D) : 0;
+  g.last = REVERSE ? seg == 0 : seg == n - 1;
+  g.slot = cut ? rest : -1;
   return g;
 }
 // The state a segment starts from (NULL: zero).
 __device__ __forceinline__ const float *start_state(const Params &p, const Segment &g) {
   if (p.slots_out) return nullptr;
-  if (g.cut) return p.slots + g.slot;
+  if (g.slot >= 0) return p.slots + (long long)g.slot * (D * D);
   return p.C0 ? p.C0 + (long long)g.unit * (D * D) : nullptr;
 }
 // Where the state it ends in goes (NULL: nowhere).
 __device__ __forceinline__ float *end_state(const Params &p, const Segment &g) {
-  if (p.slots_out) return g.last ? nullptr : p.slots_out + g.slot;
+  if (p.slots_out) return g.last ? nullptr : p.slots_out + (long long)g.slot * (D * D);
   return p.C_out && g.last ? p.C_out + (long long)g.unit * (D * D) : nullptr;
 }
 

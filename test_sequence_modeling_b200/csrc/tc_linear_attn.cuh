@@ -17,6 +17,12 @@
 // Nothing of a chunk waits for the previous chunk's outputs; only the state is a chain, and its
 // step (one product, one scaling) is shorter than a chunk's products.
 //
+// Where there are more units than SMs the CTAs share the chunks of all of them evenly, each a range of
+// consecutive ones, whose ends may lie inside a unit.  A CTA begins with the head of the unit that its
+// range ends in and hands the state on through memory; the tail of the unit that its range begins in
+// comes last, when the CTA before it has handed its state on long ago.  A CTA's number is a ticket
+// taken at its start, so the one before it has started, and what it waits for waits for nothing.
+//
 // Why so: a chunk's 64 KB of HBM traffic take an SM 2860 cycles at the measured copy rate.  The
 // products take 1580 of them: measured back to back, a product with K = 16 takes N / 2 cycles for
 // N >= 128 whatever M is, and for N = 64 37 cycles with M = 64 or A in tensor memory, 52 else.  The
@@ -64,7 +70,8 @@ constexpr uint32_t OFF_CT = OFF_PA + CHUNK * 4;    // gamma^31 .. gamma^0 (rever
 constexpr uint32_t OFF_BAR = OFF_CT + 32 * 4;
 constexpr uint32_t OFF_TSLOT = OFF_BAR + 32 * 8;
 constexpr uint32_t OFF_ABORT = OFF_TSLOT + 4;
-constexpr uint32_t SMEM_USED = OFF_ABORT + 4;
+constexpr uint32_t OFF_NUMBER = OFF_ABORT + 4;
+constexpr uint32_t SMEM_USED = OFF_NUMBER + 4;
 constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024, "one CTA's shared memory");
 
@@ -152,12 +159,46 @@ __device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint32_t step_a, u
   for (int k = 0; k < N; ++k) umma_ss_w(d, a + k * (step_a >> 4), b + k * (step_b >> 4), id, k > 0);
 }
 
+// A state handed from CTA j - 1 to CTA j: each of the four state warps counts in once it has written.
+__device__ __forceinline__ void hand_on(int *flag) {
+  __threadfence();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    __threadfence();
+    atomicAdd(flag, 1);
+  }
+}
+__device__ __forceinline__ bool wait_handed(const int *flag, volatile int *abort) {
+  const long long t0 = clock64();
+  for (;;) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+    if (__all_sync(0xffffffffu, v == 4)) return true;
+    const bool late = clock64() - t0 > WAIT_LIMIT;
+    if (__any_sync(0xffffffffu, late || *abort)) {
+      if (late && !*abort) {
+        *abort = 1;
+        record_device_error(-5 /* TTT_ERR_TIMEOUT */);
+      }
+      return false;
+    }
+    __nanosleep(200);
+  }
+}
+
+// What the CTAs share evenly, where steps > 0: `steps` chunks of each of `units` units.  ticket[0] counts
+// the CTAs, ticket[1 + j] the state that CTA j hands on in slot j; all zero before the launch.
+struct Shared {
+  int units, steps;
+  int *ticket;
+};
+
 // STATE_ONLY: the segments' own states (y and w alone).
 template <bool REVERSE, bool STATE_ONLY>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY,
                    const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmOut, const Params p,
-                   const int inject_timeout) {
+                   const Shared shared, const int inject_timeout) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(sm);
@@ -186,23 +227,57 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(tslot, TMEM_COLS);
     tmem_relinquish();
   }
+  int *number = reinterpret_cast<int *>(sm + OFF_NUMBER);
+  if (tid == 0) *number = shared.steps ? atomicAdd(shared.ticket, 1) : (int)blockIdx.x;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tb = *tslot;  // all columns are this CTA's: the base is 0, which the roles take as a constant
 
-  // This CTA's segments, their tokens and chunks.
-  const int k0 = p.first_segment + blockIdx.x, k1 = p.first_segment + p.segments;
+  // This CTA's segments, one after the other, their tokens and chunks.
+  const int cta = *number;
+  int unit_a = 0, step_a = 0, unit_b = 0, step_b = 0;  // the ends of its range
+  if (shared.steps) {
+    const long long total = (long long)shared.units * shared.steps;
+    const long long a = total * cta / gridDim.x, b = total * (cta + 1) / gridDim.x;
+    unit_a = (int)(a / shared.steps), step_a = (int)(a - (long long)unit_a * shared.steps);
+    unit_b = (int)(b / shared.steps), step_b = (int)(b - (long long)unit_b * shared.steps);
+  }
   struct Segment : lattn::Segment {
     int n, nchunks;
+    int hand_to;  // the slot of the state that it hands on, or -1
   };
-  auto segment = [&](int k) {
-    Segment g;
-    static_cast<lattn::Segment &>(g) = lattn::segment_of<REVERSE>(p, k);
+  auto segment = [&](int idx, Segment &g) {
+    g.hand_to = -1;
+    if (!shared.steps) {
+      const int k = cta + idx * (int)gridDim.x;
+      if (k >= p.segments) return false;
+      static_cast<lattn::Segment &>(g) = lattn::segment_of<REVERSE>(p, p.first_segment + k);
+    } else {
+      const int whole0 = step_a ? unit_a + 1 : unit_a;
+      const int k = idx - (step_b ? 1 : 0) + whole0;
+      int lo = 0, hi = shared.steps;
+      if (step_b && idx == 0) {
+        g.unit = unit_b;
+        hi = step_b;
+        g.hand_to = cta;
+      } else if (k < unit_b) {
+        g.unit = k;
+      } else if (k == unit_b && step_a) {
+        g.unit = unit_a;
+        lo = step_a;
+      } else {
+        return false;
+      }
+      g.t_lo = (REVERSE ? shared.steps - hi : lo) * CHUNK;
+      g.rows = min((REVERSE ? shared.steps - lo : hi) * CHUNK, p.T) - g.t_lo;
+      g.last = hi == shared.steps;
+      g.slot = lo ? cta - 1 : -1;
+    }
     g.n = min(max(lattn::sequence_length(p.lengths, g.unit / p.H, p.T) - g.t_lo, 0), g.rows);
     if (STATE_ONLY && g.last) g.n = 0;  // no segment follows it: its own state has no reader
     g.nchunks = (g.n + CHUNK - 1) / CHUNK;
-    return g;
+    return true;
   };
   auto chunk_start = [](const Segment &g, int c) { return (REVERSE ? g.nchunks - 1 - c : c) * CHUNK; };
   auto log_decay = [&](const Segment &g) { return p.log_decay[g.unit % p.H]; };
@@ -214,8 +289,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---- loads -------------------------------------------------------------------
     if (lane == 0) {
       int i = 0;
-      for (int k = k0; ok && k < k1; k += gridDim.x) {
-        const Segment g = segment(k);
+      Segment g;
+      for (int k = 0; ok && segment(k, g); ++k) {
         for (int c = 0; ok && c < g.nchunks; ++c, ++i) {
           const int slot = i & 1, t0 = g.t_lo + chunk_start(g, c);
           const uint32_t par = (uint32_t)(i / 2 - 1) & 1u;
@@ -249,7 +324,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr uint32_t ID_PW = idesc_bf16_f32(128, 64, false, true, false);
     constexpr uint32_t ID_M = idesc_bf16_f32(64, 192, true, true, false);
     int total = 0;
-    for (int k = k0; k < k1; k += gridDim.x) total += segment(k).nchunks;
+    Segment g;
+    for (int k = 0; segment(k, g); ++k) total += g.nchunks;
     auto scores = [&](int i) {  // P of chunk i, once its tiles are in
       const uint32_t slot = i & 1, par = (uint32_t)(i >> 1) & 1u;
       if (!wait_warp(&bars[FX + slot], par, abort) || !wait_warp(&bars[FY + slot], par, abort)) return false;
@@ -309,8 +385,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int half = (warp - 4) >> 2, ptid = tid - 128;
     const uint32_t row = tmem_addr(0, 32 * w4, T_P), dst = tmem_addr(0, 32 * w4, T_PB);
     int i = 0;
-    for (int k = k0; k < k1; k += gridDim.x) {
-      const Segment g = segment(k);
+    Segment g;
+    for (int k = 0; segment(k, g); ++k) {
       if (g.nchunks == 0) continue;
       const float ld = log_decay(g);
       named_barrier_sync(NB_P, 256);  // the last segment's tables are read
@@ -381,8 +457,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int s = 32 * w4 + lane;
     const uint32_t row = sw128_offset(s, 0);  // piece q of the row is at row ^ (16 q)
     int i = 0;
-    for (int k = k0; ok && k < k1; k += gridDim.x) {
-      const Segment g = segment(k);
+    Segment g;
+    for (int k = 0; ok && segment(k, g); ++k) {
       const float ld = log_decay(g);
       const float h_full = p.e * decay_pow(ld, REVERSE ? s + 1 : CHUNK - 1 - s);
       for (int c = 0; ok && c < g.nchunks; ++c, ++i) {
@@ -441,17 +517,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     // C[4 j + {2, 3}].
     const int row = 16 * w4 + (lane >> 2), col = 2 * (lane & 3);
     int i = 0;
-    for (int k = k0; ok && k < k1; k += gridDim.x) {
-      const Segment g = segment(k);
+    Segment g;
+    for (int k = 0; ok && segment(k, g); ++k) {
       const float ld = log_decay(g);
       const float d_full = decay_pow(ld, CHUNK);
       float C[32];
       {
+        if (shared.steps && g.slot >= 0 && !(ok = wait_handed(shared.ticket + 1 + g.slot, abort))) break;
         const float *C0 = lattn::start_state(p, g);
+        const bool as_is = p.transposed || (shared.steps && g.slot >= 0);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int r = row + 8 * ((e >> 1) & 1), cc = 8 * (e >> 2) + col + (e & 1);
-          C[e] = C0 ? (p.transposed ? C0[r * D + cc] : C0[cc * D + r]) : 0.f;
+          C[e] = C0 ? __ldcg(C0 + (as_is ? r * D + cc : cc * D + r)) : 0.f;
         }
       }
       for (int c = 0; c < g.nchunks; ++c, ++i) {
@@ -490,7 +568,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      if (float *Co = lattn::end_state(p, g)) {
+      // (A state handed on lies as this kernel carries it, C^T.)
+      if (g.hand_to >= 0) {
+        float *Co = p.slots + (long long)g.hand_to * (D * D);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) Co[(row + 8 * ((e >> 1) & 1)) * D + 8 * (e >> 2) + col + (e & 1)] = C[e];
+        hand_on(shared.ticket + 1 + g.hand_to);
+      } else if (float *Co = lattn::end_state(p, g)) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) Co[(8 * (e >> 2) + col + (e & 1)) * D + row + 8 * ((e >> 1) & 1)] = C[e];
       }
@@ -499,8 +583,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---- outputs --------------------------------------------------------------------
     const int t = 32 * w4 + lane;
     int i = 0;
-    for (int k = k0; k < k1; k += gridDim.x) {
-      const Segment g = segment(k);
+    Segment g;
+    for (int k = 0; segment(k, g); ++k) {
       const float ld = log_decay(g);
       const float f_full = p.c * decay_pow(ld, REVERSE ? CHUNK - 1 - t : t + 1);
       for (int c = 0; c < g.nchunks; ++c, ++i) {

@@ -49,6 +49,7 @@ std::atomic<int> g_path{TTT_PATH_AUTO};
 std::atomic<long long> g_launches{0};
 std::atomic<int> g_inject_timeout{0};
 
+size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct Range {
@@ -739,17 +740,23 @@ int check_buffers(std::initializer_list<Buffer> ins, std::initializer_list<Buffe
   return TTT_OK;
 }
 
-// How the units (batch x heads) are dealt out to the SMs, one segment an SM at a time.  Whole units
-// fill rounds of all SMs; those that would be left for a last, unfilled round (or all of them where
-// there are fewer units than SMs) may be cut into segments that fill it, which costs a pass over half
-// of their inputs for the segments' own states.  The cut with the least time is taken, in steps of
-// one chunk on one SM: `passes` passes of ceil(segments / SMs) rounds each and as many state passes as
-// the call needs, a step of which takes ATTN_STATE_STEP of a full one, ATTN_SEGMENT_STEPS for each
-// segment's start and end, and ATTN_CUT_STEPS for the two more launches of a state pass.  Measured on one B200 (forward, bf16): B16 H12 T2048, 44 of 192 units
-// cut in three, against none cut; B1 H32 T32768 cut in nine, against four (see the kernel's table).
+// How the units (batch x heads) are dealt out to the SMs.
+//
+// More units than SMs, tensor-core kernel: the CTAs share all chunks evenly (`steps` chunks a unit, see
+// tc_linear_attn.cuh), unless whole units come out even.  Measured on one B200 against whole units
+// alone: see there.
+//
+// Fewer units than SMs (and what would be left for the last, unfilled round of the CUDA-core kernel): they
+// may be cut into segments that fill the SMs, which costs a pass over half of their inputs for the
+// segments' own states.  The cut with the least time is taken, in steps of one chunk on one SM: each of
+// the call's passes takes ceil(segments / SMs) rounds, as does each of its state passes, a step of which
+// takes ATTN_STATE_STEP of a full one; ATTN_SEGMENT_STEPS go to each segment's start and end and
+// ATTN_CUT_STEPS to the two more launches of a state pass.
 struct AttnPlan {
   lattn::Cut cut;
-  size_t slots_bytes;  // one set of segment states
+  int steps;           // > 0: the CTAs share the chunks
+  size_t slots_bytes;  // one set of segment states, or the states that CTAs hand on
+  size_t ticket_bytes; // one pass's counters, after the slots
 };
 constexpr int ATTN_SMS = 148;          // SMs of a B200: the workspace size does not ask a device
 constexpr int ATTN_CHUNK = 128;        // tokens of a step
@@ -757,10 +764,17 @@ constexpr int ATTN_MOST_SEGMENTS = 64;
 constexpr double ATTN_STATE_STEP = 0.55;
 constexpr double ATTN_SEGMENT_STEPS = 0.7;
 constexpr double ATTN_CUT_STEPS = 4;
-AttnPlan attn_plan(long long units, int T, bool backward) {
-  AttnPlan best{{(int)units, 1, T > 0 ? T : 1}, 0};
+static_assert(ATTN_CHUNK == tclattn::CHUNK && ATTN_CHUNK % lattn::CHUNK == 0, "segments are whole chunks");
+AttnPlan attn_plan(long long units, int T, bool backward, bool tensor_cores) {
+  AttnPlan best{{(int)units, 1, T > 0 ? T : 1}, 0, 0, 0};
   const long long left = units % ATTN_SMS, chunks = ((long long)T + ATTN_CHUNK - 1) / ATTN_CHUNK;
   if (left == 0 || chunks < 2) return best;
+  if (tensor_cores && units > ATTN_SMS) {
+    best.steps = (int)chunks;
+    best.slots_bytes = (size_t)ATTN_SMS * lattn::D * lattn::D * 4;
+    best.ticket_bytes = (size_t)align16(4 * (1 + ATTN_SMS));
+    return best;
+  }
   const int passes = backward ? 3 : 1, states = backward ? 2 : 1;
   auto rounds = [](long long n) { return (double)((n + ATTN_SMS - 1) / ATTN_SMS); };
   double least = passes * (chunks + ATTN_SEGMENT_STEPS);
@@ -778,6 +792,10 @@ AttnPlan attn_plan(long long units, int T, bool backward) {
   }
   return best;
 }
+// Forward: slots, counters.  Backward: two sets of slots, three passes' counters.
+size_t attn_workspace(const AttnPlan &plan, bool backward) {
+  return plan.slots_bytes * (backward ? 2 : 1) + plan.ticket_bytes * (backward ? 3 : 1);
+}
 
 template <typename KernelT, typename ParamsT>
 int launch_attn(KernelT kernel, long long grid, int threads, size_t smem, cudaStream_t s, const ParamsT &p) {
@@ -791,7 +809,7 @@ int launch_attn(KernelT kernel, long long grid, int threads, size_t smem, cudaSt
 }
 
 template <bool REVERSE, bool STATE_ONLY>
-int launch_attn_tc(long long units, const lattn::Params &p, cudaStream_t s) {
+int launch_attn_tc(long long units, const lattn::Params &p, int steps, int *ticket, cudaStream_t s) {
   CUtensorMap mx, my, mw, mo;
   if (!make_qkv_map(&my, p.Y, p.T, units, tclattn::CHUNK) || !make_qkv_map(&mw, p.W, p.T, units, tclattn::CHUNK) ||
       !make_qkv_map(&mx, STATE_ONLY ? p.Y : p.X, p.T, units, tclattn::CHUNK) ||
@@ -801,21 +819,24 @@ int launch_attn_tc(long long units, const lattn::Params &p, cudaStream_t s) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tclattn::SMEM_BYTES) != cudaSuccess)
     return TTT_ERR_CUDA;
   kernel<<<(unsigned)std::min(p.segments, ATTN_SMS), tclattn::THREADS, tclattn::SMEM_BYTES, s>>>(
-      mx, my, mw, mo, p, g_inject_timeout.load());
+      mx, my, mw, mo, p, tclattn::Shared{(int)units, steps, ticket}, g_inject_timeout.load());
   if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return TTT_OK;
 }
 
-// One pass over all units (or, without an output, over the cut ones): bf16 on the tensor cores (unless
-// the CUDA-core path is selected), everything else by lattn::attn_kernel.
-int attn_pass(bool bf16, bool reverse, long long units, lattn::Params p, cudaStream_t s) {
+bool attn_on_tensor_cores(bool bf16, int T) { return bf16 && T > 0 && g_path.load() != TTT_PATH_SIMT; }
+
+// One pass over all units (or, for states alone, over the cut ones).  A shared pass takes zeroed counters.
+int attn_pass(bool bf16, bool tc, bool reverse, long long units, lattn::Params p, int steps, int *ticket,
+              cudaStream_t s) {
   const bool state_only = p.slots_out != nullptr;
   p.first_segment = state_only ? p.cut.whole : 0;
   p.segments = p.cut.segments((int)units) - p.first_segment;
-  if (bf16 && p.T > 0 && g_path.load() != TTT_PATH_SIMT) {
-    if (state_only) return reverse ? launch_attn_tc<true, true>(units, p, s) : launch_attn_tc<false, true>(units, p, s);
-    return reverse ? launch_attn_tc<true, false>(units, p, s) : launch_attn_tc<false, false>(units, p, s);
+  if (tc) {
+    auto run = state_only ? (reverse ? launch_attn_tc<true, true> : launch_attn_tc<false, true>)
+                          : (reverse ? launch_attn_tc<true, false> : launch_attn_tc<false, false>);
+    return run(units, p, steps, ticket, s);
   }
   auto kernel = bf16 ? (reverse ? lattn::attn_kernel<__nv_bfloat16, true> : lattn::attn_kernel<__nv_bfloat16, false>)
                      : (reverse ? lattn::attn_kernel<float, true> : lattn::attn_kernel<float, false>);
@@ -823,12 +844,12 @@ int attn_pass(bool bf16, bool reverse, long long units, lattn::Params p, cudaStr
 }
 
 // The states that the cut units' segments start from, into `slots`: the segments' own states, then the scan.
-int attn_segment_states(bool bf16, bool reverse, long long units, const AttnPlan &plan, const void *Y, const void *W,
+int attn_segment_states(bool bf16, bool tc, bool reverse, long long units, const AttnPlan &plan, const void *Y, const void *W,
                         float e, const float *log_decay, const int *lengths, const float *C0, int H, int T,
                         float *slots, cudaStream_t s) {
   lattn::Params p{Y, Y, W, log_decay, lengths, nullptr, nullptr, false, 0.f, 0.f, e, nullptr, nullptr, slots, H, T,
                   plan.cut, 0, 0};
-  int st = attn_pass(bf16, reverse, units, p, s);
+  int st = attn_pass(bf16, tc, reverse, units, p, 0, nullptr, s);
   if (st != TTT_OK) return st;
   lattn::ScanParams sp{slots, C0, log_decay, lengths, H, T, plan.cut};
   return launch_attn(reverse ? lattn::scan_kernel<true> : lattn::scan_kernel<false>, (units - plan.cut.whole) * 4,
@@ -856,21 +877,27 @@ int run_attn_fwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
   const bool tok = T > 0, bf16 = qkv_dtype == TTT_BF16;
   if (g_path.load() == TTT_PATH_TC && !bf16) return TTT_ERR_UNSUPPORTED;
   const size_t xb = (size_t)units * T * d * (bf16 ? 2 : 4), sb = (size_t)units * d * d * 4;
-  const AttnPlan plan = attn_plan(units, T, false);
-  if (plan.slots_bytes && (!workspace || workspace_bytes < plan.slots_bytes)) return TTT_ERR_ARG;
+  const bool tc = attn_on_tensor_cores(bf16, T);
+  const AttnPlan plan = attn_plan(units, T, false, tc);
+  const size_t wb = attn_workspace(plan, false);
+  if (wb && (!workspace || workspace_bytes < wb)) return TTT_ERR_ARG;
   st = check_buffers({{Q, xb, tok}, {K, xb, tok}, {V, xb, tok}, {log_decay, (size_t)H * 4, true}, {S0, sb, false},
                       {lengths, (size_t)B * 4, false}},
-                     {{Z, xb, tok}, {S_out, sb, false}, {plan.slots_bytes ? workspace : nullptr, plan.slots_bytes, false}});
+                     {{Z, xb, tok}, {S_out, sb, false}, {wb ? workspace : nullptr, wb, false}});
   if (st != TTT_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float *slots = static_cast<float *>(workspace);
-  if (plan.slots_bytes) {
-    st = attn_segment_states(bf16, false, units, plan, K, V, 1.f, log_decay, lengths, S0, H, T, slots, s);
+  int *ticket = nullptr;
+  if (plan.steps) {
+    ticket = reinterpret_cast<int *>(slots + plan.slots_bytes / 4);
+    if (cudaMemsetAsync(ticket, 0, plan.ticket_bytes, s) != cudaSuccess) return TTT_ERR_CUDA;
+  } else if (plan.slots_bytes) {
+    st = attn_segment_states(bf16, tc, false, units, plan, K, V, 1.f, log_decay, lengths, S0, H, T, slots, s);
     if (st != TTT_OK) return st;
   }
   lattn::Params p{Q, K, V, log_decay, lengths, S0, slots, false, scale, scale, 1.f, Z, S_out, nullptr, H, T,
                   plan.cut, 0, 0};
-  return attn_pass(bf16, false, units, p, s);
+  return attn_pass(bf16, tc, false, units, p, plan.steps, ticket, s);
 }
 
 int run_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype, const float *log_decay, const float *S0,
@@ -883,8 +910,9 @@ int run_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
   const bool tok = T > 0, bf16 = qkv_dtype == TTT_BF16;
   if (g_path.load() == TTT_PATH_TC && !bf16) return TTT_ERR_UNSUPPORTED;
   const size_t xb = (size_t)units * T * d * (bf16 ? 2 : 4), sb = (size_t)units * d * d * 4;
-  const AttnPlan plan = attn_plan(units, T, true);
-  const size_t wb = 2 * plan.slots_bytes;
+  const bool tc = attn_on_tensor_cores(bf16, T);
+  const AttnPlan plan = attn_plan(units, T, true, tc);
+  const size_t wb = attn_workspace(plan, true);
   if (wb && (!workspace || workspace_bytes < wb)) return TTT_ERR_ARG;
   st = check_buffers({{Q, xb, tok}, {K, xb, tok}, {V, xb, tok}, {dZ, xb, tok}, {log_decay, (size_t)H * 4, true},
                       {S0, sb, false}, {dS_T, sb, false}, {lengths, (size_t)B * 4, false}},
@@ -892,11 +920,16 @@ int run_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
   if (st != TTT_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float *slots_s = static_cast<float *>(workspace), *slots_g = nullptr;
-  if (plan.slots_bytes) {
-    slots_g = slots_s + plan.slots_bytes / 4;
-    st = attn_segment_states(bf16, false, units, plan, K, V, 1.f, log_decay, lengths, S0, H, T, slots_s, s);
+  int *ticket[3] = {};
+  if (plan.slots_bytes) slots_g = slots_s + plan.slots_bytes / 4;
+  if (plan.steps) {
+    char *at = reinterpret_cast<char *>(slots_g) + plan.slots_bytes;
+    for (int i = 0; i < 3; ++i) ticket[i] = reinterpret_cast<int *>(at + i * plan.ticket_bytes);
+    if (cudaMemsetAsync(at, 0, 3 * plan.ticket_bytes, s) != cudaSuccess) return TTT_ERR_CUDA;
+  } else if (plan.slots_bytes) {
+    st = attn_segment_states(bf16, tc, false, units, plan, K, V, 1.f, log_decay, lengths, S0, H, T, slots_s, s);
     if (st != TTT_OK) return st;
-    st = attn_segment_states(bf16, true, units, plan, Q, dZ, scale, log_decay, lengths, dS_T, H, T, slots_g, s);
+    st = attn_segment_states(bf16, tc, true, units, plan, Q, dZ, scale, log_decay, lengths, dS_T, H, T, slots_g, s);
     if (st != TTT_OK) return st;
   }
   lattn::Params pq{dZ, V, K, log_decay, lengths, S0, slots_s, true, scale, scale, 1.f, dQ, nullptr, nullptr, H, T,
@@ -906,10 +939,10 @@ int run_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
   lattn::Params pv{K, Q, dZ, log_decay, lengths, dS_T, slots_g, false, scale, 1.f, scale, dV, dS0, nullptr, H, T,
                    plan.cut, 0, 0};
   if (tok) {
-    if ((st = attn_pass(bf16, false, units, pq, s)) != TTT_OK) return st;
-    if ((st = attn_pass(bf16, true, units, pk, s)) != TTT_OK) return st;
+    if ((st = attn_pass(bf16, tc, false, units, pq, plan.steps, ticket[0], s)) != TTT_OK) return st;
+    if ((st = attn_pass(bf16, tc, true, units, pk, plan.steps, ticket[1], s)) != TTT_OK) return st;
   }
-  return attn_pass(bf16, true, units, pv, s);
+  return attn_pass(bf16, tc, true, units, pv, plan.steps, ticket[2], s);
 }
 
 // The rotary arguments of a call.  TTT_OK and rotary_dim == 0: no rotation.
@@ -1385,7 +1418,10 @@ int ttt_linear_ln_decode(const void *q, const void *k, const void *v, int qkv_dt
 
 size_t ttt_linear_attn_workspace_bytes(int B, int H, int T, int d, int backward) {
   if (B < 0 || H < 0 || T < 0 || check_attn_sizes(TTT_F32, 1.f, B, H, T, d) != TTT_OK) return 0;
-  return attn_plan((long long)B * H, T, backward != 0).slots_bytes * (backward ? 2 : 1);
+  const long long units = (long long)B * H;
+  // Enough for either kernel: which one runs depends on the inputs' type and the path setting too.
+  return std::max(attn_workspace(attn_plan(units, T, backward != 0, true), backward != 0),
+                  attn_workspace(attn_plan(units, T, backward != 0, false), backward != 0));
 }
 
 int ttt_linear_attn_fwd(const void *Q, const void *K, const void *V, int qkv_dtype, const float *log_decay,
