@@ -24,5 +24,6 @@ def __getattr__(name):
                 "ttt_linear_attn_fwd", "ttt_linear_attn_bwd", "ttt_linear_attn_decode",
                 "linear_attn_workspace_bytes", "ttt_rope", "Rope", "rope_frequencies"):
         from . import ttt
-        return getattr(ttt, name)
+        value = globals()[name] = getattr(ttt, name)  # found without this function from now on
+        return value
     raise AttributeError(name)

@@ -14,7 +14,7 @@ import math
 import torch
 
 from . import _lib
-from ._lib import TTT_BF16, TTT_F32, TTTError, check  # noqa: F401
+from ._lib import TTT_BF16, TTT_F32, TTT_OK, TTTError, check  # noqa: F401
 
 _QKV_DTYPES = {torch.float32: TTT_F32, torch.bfloat16: TTT_BF16}
 
@@ -60,8 +60,22 @@ def _out(t, shape, device, name):
 
 
 def _stream(stream, device):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes_stream(s)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)  # torch.cuda.current_stream without its object
+    return ctypes_stream(stream)
+
+
+def _call(name, device, *args):
+    """One library call with `device` current, which it mostly is: the switch costs a host-bound
+    call as much as the rest of it."""
+    fn = getattr(_lib.load(), name)
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = fn(*args)
+    else:
+        st = fn(*args)
+    if st != TTT_OK:
+        check(st, name)
 
 
 def ctypes_stream(s) -> int:
@@ -589,9 +603,10 @@ def _ints(t, name, shape):
 
 def _same_device(Q, *tensors):
     """The C ABI reads plain pointers of one device."""
+    device = Q.device
     for t in tensors:
-        if t is not None and t.device != Q.device:
-            raise ValueError(f"every tensor must be on {Q.device}, got {t.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"every tensor must be on {device}, got {t.device}")
 
 
 def _out_as(t, like_shape, like, name):
@@ -641,12 +656,9 @@ def ttt_rope(Q, K, rope, positions=None, first_position=0, inverse=False, Q_out=
     strides = ctypes.c_longlong * 3
     sq = strides(*Q.stride()[:3])
     sk = strides(*K.stride()[:3]) if K is not None else None
-    with torch.cuda.device(Q.device):
-        st = _lib.load().ttt_rope(_ptr(Q), _ptr(K), _QKV_DTYPES[Q.dtype], _ptr(positions), int(first_position),
-                                  _ptr(rope.inv_freq), rope.rotary, int(rope.interleaved), rope.mscale,
-                                  int(bool(inverse)), B, Hq, Hk, T, d, sq, sk, _ptr(Q_out), _ptr(K_out),
-                                  _stream(stream, Q.device))
-    check(st, "ttt_rope")
+    _call("ttt_rope", Q.device, _ptr(Q), _ptr(K), _QKV_DTYPES[Q.dtype], _ptr(positions), int(first_position),
+          _ptr(rope.inv_freq), rope.rotary, int(rope.interleaved), rope.mscale, int(bool(inverse)), B, Hq, Hk, T, d, sq,
+          sk, _ptr(Q_out), _ptr(K_out), _stream(stream, Q.device))
     return Q_out, K_out
 
 
@@ -693,11 +705,8 @@ def ttt_linear_attn_fwd(Q, K, V, log_decay, scale=None, S0=None, lengths=None, r
     Z = _out_as(Z, (B, H, T, d), Q, "Z")
     S_out = _out(S_out, (B, H, d, d), Q.device, "S_out")
     _same_device(Q, Z, S_out)
-    with torch.cuda.device(Q.device):
-        st = _lib.load().ttt_linear_attn_fwd(_ptr(Q), _ptr(K), _ptr(V), dt, _ptr(log_decay), _ptr(S0), _ptr(lengths),
-                                             scale, B, H, T, d, _ptr(Z), _ptr(S_out), *_ws(workspace),
-                                             _stream(stream, Q.device))
-    check(st, "ttt_linear_attn_fwd")
+    _call("ttt_linear_attn_fwd", Q.device, _ptr(Q), _ptr(K), _ptr(V), dt, _ptr(log_decay), _ptr(S0), _ptr(lengths),
+          scale, B, H, T, d, _ptr(Z), _ptr(S_out), *_ws(workspace), _stream(stream, Q.device))
     return Z, S_out
 
 
@@ -720,12 +729,9 @@ def ttt_linear_attn_bwd(Q, K, V, log_decay, dZ, scale=None, S0=None, dS_T=None, 
     _same_device(Q, dZ, dS_T)
     out = {n: torch.empty_like(Q) for n in ("dQ", "dK", "dV")}
     out["dS0"] = torch.empty(B, H, d, d, device=Q.device)
-    with torch.cuda.device(Q.device):
-        st = _lib.load().ttt_linear_attn_bwd(_ptr(Q), _ptr(K), _ptr(V), dt, _ptr(log_decay), _ptr(S0), _ptr(lengths),
-                                             scale, _ptr(dZ), _ptr(dS_T), B, H, T, d, _ptr(out["dQ"]),
-                                             _ptr(out["dK"]), _ptr(out["dV"]), _ptr(out["dS0"]), *_ws(workspace),
-                                             _stream(stream, Q.device))
-    check(st, "ttt_linear_attn_bwd")
+    _call("ttt_linear_attn_bwd", Q.device, _ptr(Q), _ptr(K), _ptr(V), dt, _ptr(log_decay), _ptr(S0), _ptr(lengths),
+          scale, _ptr(dZ), _ptr(dS_T), B, H, T, d, _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(out["dS0"]),
+          *_ws(workspace), _stream(stream, Q.device))
     if rope is not None:
         out["dQ"], out["dK"] = ttt_rope(out["dQ"], out["dK"], rope, positions=positions, inverse=True, stream=stream)
     return out
@@ -753,13 +759,10 @@ def ttt_linear_attn_decode(q, k, v, log_decay, S, scale=None, rope=None, positio
     z = _out_as(z, (B, H, d), q, "z")
     inv_freq = None if rope is None else rope.inv_freq
     _same_device(q, k, v, log_decay, S, positions, inv_freq, z)
-    with torch.cuda.device(q.device):
-        st = _lib.load().ttt_linear_attn_decode(
-            _ptr(q), _ptr(k), _ptr(v), _QKV_DTYPES[q.dtype], _ptr(log_decay), float(d ** -0.5 if scale is None else scale),
-            _ptr(S), _ptr(positions), _ptr(inv_freq), 0 if rope is None else rope.rotary,
-            0 if rope is None else int(rope.interleaved), 1.0 if rope is None else rope.mscale, B, H, d, _ptr(z),
-            _stream(stream, q.device))
-    check(st, "ttt_linear_attn_decode")
+    _call("ttt_linear_attn_decode", q.device, _ptr(q), _ptr(k), _ptr(v), _QKV_DTYPES[q.dtype], _ptr(log_decay),
+          float(d ** -0.5 if scale is None else scale), _ptr(S), _ptr(positions), _ptr(inv_freq),
+          0 if rope is None else rope.rotary, 0 if rope is None else int(rope.interleaved),
+          1.0 if rope is None else rope.mscale, B, H, d, _ptr(z), _stream(stream, q.device))
     return z
 
 

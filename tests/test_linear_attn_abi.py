@@ -80,13 +80,21 @@ def test_backward_refuses_its_own_arguments(lib):
 
 def test_workspace_rule(lib):
     size = lib.ttt_linear_attn_workspace_bytes
-    # Enough units, short sequences, or nothing: no segments.
-    for B, H, T in ((16, 12, 2048), (1, 1, 512), (0, 3, 4096), (3, 3, 0), (148, 1, 1 << 20)):
+    state, counters = 64 * 64 * 4, 608  # a state; one pass's counters (1 + 148 ints, rounded to 16 bytes)
+    # Whole rounds of units on 148 SMs, one chunk of 128 tokens, or nothing: nothing to share or cut.
+    for B, H, T in ((148, 1, 1 << 20), (148, 2, 300), (16, 12, 128), (1, 1, 128), (0, 3, 4096), (3, 3, 0)):
         assert size(B, H, T, 64, 0) == 0 and size(B, H, T, 64, 1) == 0, (B, H, T)
-    for B, H, T in ((1, 1, 513), (1, 32, 32768), (1, 1, 1 << 30), (6, 8, 1999), (147, 1, 1 << 20)):
-        n, odd = divmod(size(B, H, T, 64, 0), B * H * 16384)
-        assert odd == 0 and n * B * H <= 2 * 148 + B * H and n != 1, (B, H, T, n)
-        assert size(B, H, T, 64, 1) == 2 * size(B, H, T, 64, 0)
+    # More units than SMs: 148 states to hand on and a pass's counters (or, for the CUDA-core kernel, the
+    # segments of a last round, if more).
+    for B, H, T in ((16, 12, 2048), (149, 1, 129), (16, 32, 8192)):
+        fwd, bwd = 148 * state + counters, 2 * 148 * state + 3 * counters
+        assert size(B, H, T, 64, 0) >= fwd and size(B, H, T, 64, 1) >= bwd, (B, H, T)
+    # Fewer: at most 64 segments a unit, at least two.
+    for B, H, T in ((1, 1, 2000), (1, 32, 32768), (1, 1, 1 << 30), (6, 8, 1999)):
+        n, odd = divmod(size(B, H, T, 64, 0), B * H * state)
+        assert odd == 0 and 2 <= n <= 64, (B, H, T, n)
+        n, odd = divmod(size(B, H, T, 64, 1), 2 * B * H * state)
+        assert odd == 0 and 2 <= n <= 64, (B, H, T, n)
     assert size(-1, 2, 3, 64, 0) == 0 and size(1, 2, 3000, 32, 0) == 0
 
 
