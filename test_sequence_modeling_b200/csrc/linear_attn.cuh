@@ -40,7 +40,8 @@ using simt::D;
 using simt::load_in;
 
 constexpr int CHUNK = 64;
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
+constexpr int STEP_THREADS = 256;  // of the single-token step
 constexpr int LD = D + 4;  // padded row stride: 8 rows' float4 at one column hit 8 distinct bank groups
 
 // How the units' sequences are dealt out to segments: units below `whole` are one segment each, the others are
@@ -121,23 +122,59 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// acc += x (u, v): one row of an 8 x 8 register tile, columns 4 tx .. and 32 + 4 tx ...
+__device__ __forceinline__ void row_times(float (&acc)[8], float x, float4 u, float4 v) {
+  acc[0] = fmaf(x, u.x, acc[0]);
+  acc[1] = fmaf(x, u.y, acc[1]);
+  acc[2] = fmaf(x, u.z, acc[2]);
+  acc[3] = fmaf(x, u.w, acc[3]);
+  acc[4] = fmaf(x, v.x, acc[4]);
+  acc[5] = fmaf(x, v.y, acc[5]);
+  acc[6] = fmaf(x, v.z, acc[6]);
+  acc[7] = fmaf(x, v.w, acc[7]);
+}
+__device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float component(float4 v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// acc (rows ty + 8 i, i0 <= i < i1) += A B for columns k0 .. k1 - 1 of A, rows of B: tiles in shared memory.
+template <int I0, int I1>
+__device__ __forceinline__ void rows_times_rows(float (&acc)[8][8], const float *A, const float *B, int k0, int k1, int tx,
+                                                int ty) {
+#pragma unroll 1
+  for (int k = k0; k < k1; k += 4) {
+    float4 a[8];
+#pragma unroll
+    for (int i = I0; i < I1; ++i) a[i] = lds4(A + (ty + 8 * i) * LD + k);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const float4 u = lds4(B + (k + kk) * LD + 4 * tx), v = lds4(B + (k + kk) * LD + 32 + 4 * tx);
+#pragma unroll
+      for (int i = I0; i < I1; ++i) row_times(acc[i], component(a[i], kk), u, v);
+    }
+  }
+}
+
 constexpr size_t SMEM_BYTES = sizeof(float) * (size_t)(5 * CHUNK * LD + 2 * CHUNK + 4);
 
-// One CTA takes one segment of one unit.  Each of the 64 x 64 x 64 products is a 4 x 4
-// register tile of each of 16 x 16 threads, in fp32 fused multiply-adds.
-template <typename InT, bool REVERSE>
-__global__ void __launch_bounds__(THREADS) attn_kernel(const Params p) {
+// One CTA takes one segment of one unit, in fp32 fused multiply-adds.  Its two halves of 64 threads hold
+// an 8 x 8 register tile of one 64 x 64 product each: the first takes m o (x y^T) and then the state's
+// y^T w, the second x C and then (m o x y^T) w on top of it, so that each does as much.  8 x 8, because with
+// 4 x 4 tiles and 256 threads the operands' reads from shared memory took twice the arithmetic's time:
+// forward B6 H8 T1999 145 us, against 121 now, of which the arithmetic is about half.
+template <typename InT, bool REVERSE, bool STATE_ONLY>
+__global__ void __launch_bounds__(THREADS, 2) attn_kernel(const Params p) {
   extern __shared__ __align__(16) float sm[];
   float *Xs = sm;                // [CHUNK][LD]
   float *Ys = Xs + CHUNK * LD;
   float *Ws = Ys + CHUNK * LD;
-  float *Ms = Ws + CHUNK * LD;   // the masked, decayed products x_t . y_s
+  float *Ms = Ws + CHUNK * LD;   // a times the masked, decayed products x_t . y_s
   float *Cs = Ms + CHUNK * LD;   // the carried state
   float *pw = Cs + D * LD;       // gamma^0 .. gamma^CHUNK
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, half = tid >> 6, tx = tid & 7, ty = (tid >> 3) & 7;
   const Segment sg = segment_of<REVERSE>(p, p.first_segment + blockIdx.x);
-  const bool state_only = p.slots_out != nullptr;
-  if (state_only && sg.last) return;
+  if (STATE_ONLY && sg.last) return;
   const float g = p.log_decay[sg.unit % p.H];
   const int len = sequence_length(p.lengths, sg.unit / p.H, p.T);
   const int n_seg = min(max(len - sg.t_lo, 0), sg.rows);  // its tokens
@@ -145,20 +182,33 @@ __global__ void __launch_bounds__(THREADS) attn_kernel(const Params p) {
   const InT *X = static_cast<const InT *>(p.X) + row0 * D;
   const InT *Y = static_cast<const InT *>(p.Y) + row0 * D;
   const InT *W = static_cast<const InT *>(p.W) + row0 * D;
-  InT *out = state_only ? nullptr : static_cast<InT *>(p.out) + row0 * D;
+  InT *out = static_cast<InT *>(p.out) + row0 * D;
 
-  // The state at the start of the pass: this thread's rows ty + 16 i, columns 4 tx .. 4 tx + 3.
-  const float *C0 = start_state(p, sg);
-  float C[4][4];
+  // The state, in registers of the first half: rows 4 ty .. and 32 + 4 ty .., columns 4 tx .. and
+  // 32 + 4 tx ...  For states alone each half takes half of the rows.
+  constexpr int ROWS = STATE_ONLY ? 4 : 8;
+  auto state_row = [&](int i) { return (STATE_ONLY ? 32 * half : 32 * (i >> 2)) + 4 * ty + (i & 3); };
+  const bool has_state = STATE_ONLY || half == 0;
+  float C[ROWS][8];
+  if (has_state) {
+    const float *C0 = start_state(p, sg);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = ty + 16 * i, col = 4 * tx + j;
-      C[i][j] = C0 ? (p.transposed ? C0[col * D + r] : C0[r * D + col]) : 0.f;
-      Cs[r * LD + col] = C[i][j];
-    }
+      for (int j = 0; j < 8; ++j) {
+        const int r = state_row(i), col = 32 * (j >> 2) + 4 * tx + (j & 3);
+        C[i][j] = C0 ? (p.transposed ? C0[col * D + r] : C0[r * D + col]) : 0.f;
+      }
   }
+  auto state_to = [&](float *to, int ld) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; j += 4)
+        *reinterpret_cast<float4 *>(to + state_row(i) * ld + 8 * j + 4 * tx) =
+            make_float4(C[i][j], C[i][j + 1], C[i][j + 2], C[i][j + 3]);
+  };
+  if (!STATE_ONLY && half == 0) state_to(Cs, LD);
   if (tid <= CHUNK) pw[tid] = decay_pow(g, tid);
 
   const int nchunks = (n_seg + CHUNK - 1) / CHUNK;
@@ -166,126 +216,115 @@ __global__ void __launch_bounds__(THREADS) attn_kernel(const Params p) {
     const int c0 = (REVERSE ? nchunks - 1 - ci : ci) * CHUNK;
     const int n = min(CHUNK, n_seg - c0);
     // Tiles: 16 lanes a row of 64 values, rows past the end as zeros.
+    const int lr = tid >> 4, lc = 4 * (tid & 15);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty + 16 * i;
+    for (int i = 0; i < CHUNK; i += THREADS / 16) {
+      const int r = lr + i;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x, w = x;
       if (r < n) {
-        const long long at = (long long)(c0 + r) * D + 4 * tx;
-        if (out) x = load4(X + at);
+        const long long at = (long long)(c0 + r) * D + lc;
+        if (!STATE_ONLY) x = load4(X + at);
         y = load4(Y + at);
         w = load4(W + at);
       }
-      *reinterpret_cast<float4 *>(Xs + r * LD + 4 * tx) = x;
-      *reinterpret_cast<float4 *>(Ys + r * LD + 4 * tx) = y;
-      *reinterpret_cast<float4 *>(Ws + r * LD + 4 * tx) = w;
+      if (!STATE_ONLY) *reinterpret_cast<float4 *>(Xs + r * LD + lc) = x;
+      *reinterpret_cast<float4 *>(Ys + r * LD + lc) = y;
+      *reinterpret_cast<float4 *>(Ws + r * LD + lc) = w;
+    }
+    if (ci + 1 < nchunks) {  // the next chunk's rows on their way to L2, 128 bytes a request
+      constexpr int LINE = 128 / (int)sizeof(InT), LINES = CHUNK * D / LINE;
+      const long long at = (long long)(REVERSE ? c0 - CHUNK : c0 + CHUNK) * D + tid * LINE;
+      if (tid < LINES && at < (long long)n_seg * D) {
+        if (!STATE_ONLY) prefetch_l2(X + at);
+        prefetch_l2(Y + at);
+        prefetch_l2(W + at);
+      }
     }
     __syncthreads();
-    if (out) {
-      // m_ts x_t . y_s for rows t = ty + 16 i, columns s = tx + 16 j.
-      float acc[4][4] = {};
+    if (!STATE_ONLY && half == 0) {
+      // a m_ts x_t . y_s for rows t = ty + 8 i, columns s = tx + 8 j; the quarter of the tile that the
+      // mask empties (i < 4 <= j; reverse: j < 4 <= i) is left out here and below.
+      float acc[8][8] = {};
+#pragma unroll 1
       for (int k = 0; k < D; k += 4) {
-        float4 x[4], y[4];
+        float4 x[8], y[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = *reinterpret_cast<const float4 *>(Xs + (ty + 16 * i) * LD + k);
-          y[i] = *reinterpret_cast<const float4 *>(Ys + (tx + 16 * i) * LD + k);
+        for (int i = 0; i < 8; ++i) {
+          x[i] = lds4(Xs + (ty + 8 * i) * LD + k);
+          y[i] = lds4(Ys + (tx + 8 * i) * LD + k);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
+          for (int j = 0; j < 8; ++j)
+            if (REVERSE ? (i < 4 || j >= 4) : (i >= 4 || j < 4))
+              acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = ty + 16 * i, s = tx + 16 * j;
-          const int gap = REVERSE ? s - t : t - s;
-          Ms[t * LD + s] = gap >= 0 ? acc[i][j] * pw[gap] : 0.f;
+        for (int j = 0; j < 8; ++j) {
+          const int t = ty + 8 * i, s = tx + 8 * j, gap = REVERSE ? s - t : t - s;
+          if (REVERSE ? (i < 4 || j >= 4) : (i >= 4 || j < 4)) Ms[t * LD + s] = gap >= 0 ? p.a * pw[gap] * acc[i][j] : 0.f;
         }
-      __syncthreads();
-      // out rows t = ty + 16 i, columns 4 tx ..: the state's part, then the chunk's own.
-      float o[4][4] = {};
-      for (int k = 0; k < D; k += 4) {
-        float4 x[4];
+      asm volatile("bar.arrive 1, %0;" ::"n"(THREADS) : "memory");
+    } else if (!STATE_ONLY) {
+      float o[8][8] = {};
+      rows_times_rows<0, 8>(o, Xs, Cs, 0, D, tx, ty);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(Xs + (ty + 16 * i) * LD + k);
+      for (int i = 0; i < 8; ++i) {
+        const int t = ty + 8 * i;
+        const float f = t < n ? p.c * pw[REVERSE ? n - 1 - t : t + 1] : 0.f;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const float4 c = *reinterpret_cast<const float4 *>(Cs + (k + kk) * LD + 4 * tx);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float xv = kk == 0 ? x[i].x : kk == 1 ? x[i].y : kk == 2 ? x[i].z : x[i].w;
-            o[i][0] = fmaf(xv, c.x, o[i][0]);
-            o[i][1] = fmaf(xv, c.y, o[i][1]);
-            o[i][2] = fmaf(xv, c.z, o[i][2]);
-            o[i][3] = fmaf(xv, c.w, o[i][3]);
-          }
-        }
+        for (int j = 0; j < 8; ++j) o[i][j] *= f;
       }
-      float in[4][4] = {};
-      for (int s = 0; s < n; s += 4) {
-        float4 m[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] = *reinterpret_cast<const float4 *>(Ms + (ty + 16 * i) * LD + s);
-#pragma unroll
-        for (int ss = 0; ss < 4; ++ss) {
-          const float4 w = *reinterpret_cast<const float4 *>(Ws + (s + ss) * LD + 4 * tx);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float mv = ss == 0 ? m[i].x : ss == 1 ? m[i].y : ss == 2 ? m[i].z : m[i].w;
-            in[i][0] = fmaf(mv, w.x, in[i][0]);
-            in[i][1] = fmaf(mv, w.y, in[i][1]);
-            in[i][2] = fmaf(mv, w.z, in[i][2]);
-            in[i][3] = fmaf(mv, w.w, in[i][3]);
-          }
-        }
+      asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");  // the first half has written m
+      if (REVERSE) {
+        rows_times_rows<0, 4>(o, Ms, Ws, 0, 32, tx, ty);
+        rows_times_rows<0, 8>(o, Ms, Ws, 32, 64, tx, ty);
+      } else {
+        rows_times_rows<0, 8>(o, Ms, Ws, 0, 32, tx, ty);
+        rows_times_rows<4, 8>(o, Ms, Ws, 32, 64, tx, ty);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = ty + 16 * i;
+      for (int i = 0; i < 8; ++i) {
+        const int t = ty + 8 * i;
         if (t < n) {
-          const float f = p.c * pw[REVERSE ? n - 1 - t : t + 1];
-          store_out(out + (long long)(c0 + t) * D + 4 * tx,
-                    make_float4(fmaf(f, o[i][0], p.a * in[i][0]), fmaf(f, o[i][1], p.a * in[i][1]),
-                                fmaf(f, o[i][2], p.a * in[i][2]), fmaf(f, o[i][3], p.a * in[i][3])));
+          InT *to = out + (long long)(c0 + t) * D + 4 * tx;
+          store_out(to, make_float4(o[i][0], o[i][1], o[i][2], o[i][3]));
+          store_out(to + 32, make_float4(o[i][4], o[i][5], o[i][6], o[i][7]));
         }
       }
     }
-    // C <- gamma^n C + e sum_s h_s y_s^T w_s for rows 4 ty .., columns 4 tx .. of the sum; the
-    // state's rows of this thread are ty + 16 i, so the products are taken there.
-    float acc[4][4] = {};
-    for (int s = 0; s < n; ++s) {
-      const float h = pw[REVERSE ? s + 1 : n - 1 - s];
-      const float4 w = *reinterpret_cast<const float4 *>(Ws + s * LD + 4 * tx);
+    if (has_state) {
+      // C <- gamma^n C + e sum_s h_s y_s^T w_s.
+      const float dn = pw[n];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float y = h * Ys[s * LD + ty + 16 * i];
-        acc[i][0] = fmaf(y, w.x, acc[i][0]);
-        acc[i][1] = fmaf(y, w.y, acc[i][1]);
-        acc[i][2] = fmaf(y, w.z, acc[i][2]);
-        acc[i][3] = fmaf(y, w.w, acc[i][3]);
+      for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) C[i][j] *= dn;
+#pragma unroll 2
+      for (int s = 0; s < n; ++s) {
+        const float h = p.e * pw[REVERSE ? s + 1 : n - 1 - s];
+        const float4 u = lds4(Ws + s * LD + 4 * tx), v = lds4(Ws + s * LD + 32 + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < ROWS; i += 4) {
+          const float4 y = lds4(Ys + s * LD + state_row(i));
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii) row_times(C[i + ii], h * component(y, ii), u, v);
+        }
       }
     }
     __syncthreads();  // every read of the state and of the tiles is done
-    const float dn = pw[n];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) C[i][j] = fmaf(dn, C[i][j], p.e * acc[i][j]);
-      *reinterpret_cast<float4 *>(Cs + (ty + 16 * i) * LD + 4 * tx) = make_float4(C[i][0], C[i][1], C[i][2], C[i][3]);
-    }
+    if (!STATE_ONLY && half == 0) state_to(Cs, LD);
   }
   // Rows behind the end.
-  if (out) {
-    for (int r = n_seg + ty; r < sg.rows; r += 16) store_out(out + (long long)r * D + 4 * tx, make_float4(0.f, 0.f, 0.f, 0.f));
+  if (!STATE_ONLY) {
+    for (int r = n_seg + (tid >> 4); r < sg.rows; r += THREADS / 16)
+      store_out(out + (long long)r * D + 4 * (tid & 15), make_float4(0.f, 0.f, 0.f, 0.f));
   }
-  if (float *Co = end_state(p, sg)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float4 *>(Co + (ty + 16 * i) * D + 4 * tx) = make_float4(C[i][0], C[i][1], C[i][2], C[i][3]);
+  if (has_state) {
+    if (float *Co = end_state(p, sg)) state_to(Co, D);
   }
 }
 
@@ -352,9 +391,9 @@ struct DecodeParams {
 };
 
 template <typename InT>
-__global__ void __launch_bounds__(THREADS) decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(STEP_THREADS) decode_kernel(const DecodeParams p) {
   __shared__ float qk[2][D];
-  __shared__ __align__(16) float part[THREADS / 32][D];
+  __shared__ __align__(16) float part[STEP_THREADS / 32][D];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
   const long long unit = blockIdx.x;
   float4 *S = reinterpret_cast<float4 *>(p.S + unit * (D * D)) + tx;
@@ -401,7 +440,7 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const DecodeParams p) {
   if (tid < D / 4) {
     float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
+    for (int w = 0; w < STEP_THREADS / 32; ++w) {
       const float4 a = *reinterpret_cast<const float4 *>(&part[w][4 * tid]);
       t.x += a.x;
       t.y += a.y;

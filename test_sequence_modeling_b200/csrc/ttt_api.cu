@@ -742,6 +742,8 @@ int check_buffers(std::initializer_list<Buffer> ins, std::initializer_list<Buffe
 
 // How the units (batch x heads) are dealt out to the SMs.
 //
+// (Segments at a time: one an SM of the tensor-core kernel, two of the CUDA-core kernel; "SMs" below.)
+//
 // More units than SMs, tensor-core kernel: the CTAs share all chunks evenly (`steps` chunks a unit, see
 // tc_linear_attn.cuh), unless whole units come out even.  Measured on one B200 against whole units
 // alone: see there.
@@ -759,6 +761,7 @@ struct AttnPlan {
   size_t ticket_bytes; // one pass's counters, after the slots
 };
 constexpr int ATTN_SMS = 148;          // SMs of a B200: the workspace size does not ask a device
+constexpr int ATTN_CUDA_CORE_CTAS = 2;  // CTAs of the CUDA-core kernel an SM
 constexpr int ATTN_CHUNK = 128;        // tokens of a step
 constexpr int ATTN_MOST_SEGMENTS = 64;
 constexpr double ATTN_STATE_STEP = 0.55;
@@ -767,7 +770,8 @@ constexpr double ATTN_CUT_STEPS = 4;
 static_assert(ATTN_CHUNK == tclattn::CHUNK && ATTN_CHUNK % lattn::CHUNK == 0, "segments are whole chunks");
 AttnPlan attn_plan(long long units, int T, bool backward, bool tensor_cores) {
   AttnPlan best{{(int)units, 1, T > 0 ? T : 1}, 0, 0, 0};
-  const long long left = units % ATTN_SMS, chunks = ((long long)T + ATTN_CHUNK - 1) / ATTN_CHUNK;
+  const long long slots = ATTN_SMS * (tensor_cores ? 1 : ATTN_CUDA_CORE_CTAS);  // segments at a time
+  const long long left = units % slots, chunks = ((long long)T + ATTN_CHUNK - 1) / ATTN_CHUNK;
   if (left == 0 || chunks < 2) return best;
   if (tensor_cores && units > ATTN_SMS) {
     best.steps = (int)chunks;
@@ -776,7 +780,7 @@ AttnPlan attn_plan(long long units, int T, bool backward, bool tensor_cores) {
     return best;
   }
   const int passes = backward ? 3 : 1, states = backward ? 2 : 1;
-  auto rounds = [](long long n) { return (double)((n + ATTN_SMS - 1) / ATTN_SMS); };
+  auto rounds = [&](long long n) { return (double)((n + slots - 1) / slots); };
   double least = passes * (chunks + ATTN_SEGMENT_STEPS);
   for (int n = 2; n <= ATTN_MOST_SEGMENTS && n <= chunks; ++n) {
     const long long len = (chunks + n - 1) / n, nseg = (chunks + len - 1) / len;
@@ -838,8 +842,13 @@ int attn_pass(bool bf16, bool tc, bool reverse, long long units, lattn::Params p
                           : (reverse ? launch_attn_tc<true, false> : launch_attn_tc<false, false>);
     return run(units, p, steps, ticket, s);
   }
-  auto kernel = bf16 ? (reverse ? lattn::attn_kernel<__nv_bfloat16, true> : lattn::attn_kernel<__nv_bfloat16, false>)
-                     : (reverse ? lattn::attn_kernel<float, true> : lattn::attn_kernel<float, false>);
+  auto kernel = [&] {
+    if (state_only)
+      return bf16 ? (reverse ? lattn::attn_kernel<__nv_bfloat16, true, true> : lattn::attn_kernel<__nv_bfloat16, false, true>)
+                  : (reverse ? lattn::attn_kernel<float, true, true> : lattn::attn_kernel<float, false, true>);
+    return bf16 ? (reverse ? lattn::attn_kernel<__nv_bfloat16, true, false> : lattn::attn_kernel<__nv_bfloat16, false, false>)
+                : (reverse ? lattn::attn_kernel<float, true, false> : lattn::attn_kernel<float, false, false>);
+  }();
   return launch_attn(kernel, p.segments, lattn::THREADS, lattn::SMEM_BYTES, s, p);
 }
 
@@ -968,7 +977,7 @@ int run_attn_decode(const void *q, const void *k, const void *v, int qkv_dtype, 
                      {{S, (size_t)units * d * d * 4, true}, {z, xb, true}});
   if (st != TTT_OK) return st;
   lattn::DecodeParams p{q, k, v, log_decay, scale, S, {inv_freq, rotary_dim, interleaved != 0, mscale}, positions, H, z};
-  return launch_attn(bf16 ? lattn::decode_kernel<__nv_bfloat16> : lattn::decode_kernel<float>, units, lattn::THREADS, 0,
+  return launch_attn(bf16 ? lattn::decode_kernel<__nv_bfloat16> : lattn::decode_kernel<float>, units, lattn::STEP_THREADS, 0,
                      static_cast<cudaStream_t>(stream), p);
 }
 
