@@ -59,7 +59,7 @@ __device__ __forceinline__ int partner_of(const Plan &plan, int j, int &pair, in
 }
 
 constexpr int THREADS = 256;
-constexpr int TILE = 16;  // tokens of a CTA
+constexpr int MOST_TILE = 16;  // tokens of a CTA at most
 
 struct Tensor {
   const void *x;
@@ -76,63 +76,63 @@ struct Params {
   float sin_sign;        // -1: inverse
   int T;
   long long tokens;      // B T
+  int tile;              // tokens of a CTA: a power of two up to MOST_TILE
   int head_groups;       // CTAs that share a tile's heads
 };
 
-enum { PAIRED = 0, INTERLEAVED = 1, ANY = 2 };
-
-template <typename InT>
-struct Vec {
-  static constexpr int N = 16 / sizeof(InT);
-  uint4 raw;
-  __device__ __forceinline__ void load(const InT *p) { raw = *reinterpret_cast<const uint4 *>(p); }
-  __device__ __forceinline__ void store(InT *p) const { *reinterpret_cast<uint4 *>(p) = raw; }
-  __device__ __forceinline__ void get(float (&f)[N]) const;
-  __device__ __forceinline__ void set(const float (&f)[N]);
+// V neighbouring values of a row, moved as one.
+template <typename InT, int V>
+struct Piece;
+template <int V>
+struct alignas(4 * V) Piece<float, V> {
+  float v[V];
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = v[i];
+  }
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = f[i];
+  }
+};
+template <int V>
+struct alignas(2 * V) Piece<__nv_bfloat16, V> {  // in words of two
+  uint32_t w[V / 2];
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+  }
 };
 template <>
-__device__ __forceinline__ void Vec<float>::get(float (&f)[4]) const {
-  f[0] = __uint_as_float(raw.x);
-  f[1] = __uint_as_float(raw.y);
-  f[2] = __uint_as_float(raw.z);
-  f[3] = __uint_as_float(raw.w);
-}
-template <>
-__device__ __forceinline__ void Vec<float>::set(const float (&f)[4]) {
-  raw = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-}
-template <>
-__device__ __forceinline__ void Vec<__nv_bfloat16>::get(float (&f)[8]) const {
-  const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
-}
-template <>
-__device__ __forceinline__ void Vec<__nv_bfloat16>::set(const float (&f)[8]) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    u[i] = *reinterpret_cast<const uint32_t *>(&h);
-  }
-  raw = make_uint4(u[0], u[1], u[2], u[3]);
-}
+struct Piece<__nv_bfloat16, 1> {
+  __nv_bfloat16 v;
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = __bfloat162float(v); }
+  __device__ __forceinline__ void set(const float (&f)[1]) { v = __float2bfloat16_rn(f[0]); }
+};
 
-// A thread takes two 16-byte pieces of a row: PAIRED (half layout, rotary / 2 whole pieces): a
-// piece and its partner; INTERLEAVED: two neighbours, whose pairs are inside; ANY (half layout
-// with a pair's values at unlike places of their pieces): two neighbours, partners read singly.
-template <typename InT, int MODE>
+// A thread takes two pieces of V values of a row.  Half layout: a piece and its partner, V the most
+// values up to 16 bytes that rotary / 2 is a multiple of (a narrower piece costs more instructions:
+// bf16, B16 H32 T2048: 87 us at V = 8; see ttt_rope's choice).  Interleaved: two neighbouring pieces of 16
+// bytes, whose pairs are inside.
+template <typename InT, int V, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
-  constexpr int N = Vec<InT>::N;
-  constexpr int ITEMS = D / N / 2;  // threads a row
-  __shared__ float2 table[TILE][D / 2];
+  constexpr int ITEMS = D / V / 2;       // threads a row
+  constexpr int ROWS = THREADS / ITEMS;  // rows a step
+  __shared__ float2 table[MOST_TILE][D / 2];
   const int tid = threadIdx.x;
-  const long long tile0 = (long long)(blockIdx.x / p.head_groups) * TILE;
+  const long long tile0 = (long long)(blockIdx.x / p.head_groups) * p.tile;
   const int group = blockIdx.x % p.head_groups;
-  const int ntok = (int)min((long long)TILE, p.tokens - tile0);
+  const int ntok = (int)min((long long)p.tile, p.tokens - tile0);
   const int half = p.plan.rotary >> 1;
   for (int x = tid; x < ntok * half; x += THREADS) {
     const int tok = x / half, i = x - tok * half;
@@ -144,84 +144,74 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
   }
   __syncthreads();
 
-  const int item = tid % ITEMS;
-  const int heads = p.t[0].heads + p.t[1].heads;
-  const int rows = ntok * heads;
-  constexpr int ROWS = THREADS / ITEMS;  // rows a step
-  const int hv = half / N;
-  int a, b;
-  bool turn = true;
-  if (MODE == PAIRED) {
-    turn = item < hv;
-    a = turn ? item : 2 * hv + 2 * (item - hv);
-    b = turn ? item + hv : a + 1;
-  } else {
-    a = 2 * item;
-    b = a + 1;
+  const int item = tid % ITEMS, r = tid / ITEMS, tok = r & (p.tile - 1);
+  if (tok >= ntok) return;
+  const long long at = tile0 + tok, bi = at / p.T, t = at - bi * p.T;
+  const int hv = half / V;
+  const bool turn = INTERLEAVED || item < hv;
+  const int a = INTERLEAVED ? 2 * item : turn ? item : 2 * hv + 2 * (item - hv);
+  const int b = !INTERLEAVED && turn ? item + hv : a + 1;
+  // The turn of this thread's V pairs: a V + i, or, interleaved, those inside the two pieces.
+  float2 cs[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int pair = INTERLEAVED ? a * (V / 2) + i : a * V + i;
+    cs[i] = turn && pair < half ? table[tok][pair] : make_float2(1.f, 0.f);
   }
-  for (int r = group * ROWS + tid / ITEMS; r < rows; r += ROWS * p.head_groups) {
-    const int h = r / ntok, tok = r - h * ntok;
-    const long long at = tile0 + tok;
-    const long long bi = at / p.T, t = at - bi * p.T;
-    const int which = h >= p.t[0].heads;
-    const Tensor &T = p.t[which];
-    const int head = which ? h - p.t[0].heads : h;
-    const InT *x = static_cast<const InT *>(T.x) + bi * T.sb + head * T.sh + t * T.st;
-    InT *y = static_cast<InT *>(T.y) + ((bi * T.heads + head) * p.T + t) * D;
-    Vec<InT> va, vb;
-    va.load(x + a * N);
-    vb.load(x + b * N);
-    if (MODE == PAIRED) {
-      if (turn) {
-        float fa[N], fb[N];
-        va.get(fa);
-        vb.get(fb);
+  using P = Piece<InT, V>;
+  auto turned = [&](P &va, P &vb) {
+    if (!turn) return;
+    float fa[V], fb[V];
+    va.get(fa);
+    vb.get(fb);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float2 cs = table[tok][a * N + i];
-          const float u = fa[i], w = fb[i];
-          fa[i] = fmaf(u, cs.x, -w * cs.y);
-          fb[i] = fmaf(w, cs.x, u * cs.y);
+    for (int i = 0; i < V; ++i) {
+      if (INTERLEAVED) {
+        constexpr int H = V / 2;
+        if (a * H + i < half) {
+          float &u = i < H ? fa[2 * (i % H)] : fb[2 * (i % H)], &w = i < H ? fa[2 * (i % H) + 1] : fb[2 * (i % H) + 1];
+          const float x = u, y = w;
+          u = fmaf(x, cs[i].x, -y * cs[i].y);
+          w = fmaf(y, cs[i].x, x * cs[i].y);
         }
-        va.set(fa);
-        vb.set(fb);
+      } else {
+        const float x = fa[i], y = fb[i];
+        fa[i] = fmaf(x, cs[i].x, -y * cs[i].y);
+        fb[i] = fmaf(y, cs[i].x, x * cs[i].y);
       }
-    } else {
+    }
+    va.set(fa);
+    vb.set(fb);
+  };
+  // This thread's heads, of Q and then of K: four at a time, whose loads do not wait for one another.
+  const int step = ROWS / p.tile * p.head_groups, h0 = group * (ROWS / p.tile) + r / p.tile;
+  constexpr int BATCH = 4;
 #pragma unroll
-      for (int which_vec = 0; which_vec < 2; ++which_vec) {
-        Vec<InT> &v = which_vec ? vb : va;
-        const int j0 = (which_vec ? b : a) * N;
-        if (j0 < p.plan.rotary) {
-          float f[N];
-          v.get(f);
-          if (MODE == INTERLEAVED) {
+  for (int which = 0; which < 2; ++which) {
+    const Tensor &T = p.t[which];
+    const InT *x = static_cast<const InT *>(T.x) + bi * T.sb + t * T.st;
+    InT *y = static_cast<InT *>(T.y) + (bi * T.heads * p.T + t) * D;
+    const long long y_head = (long long)p.T * D;
+    for (int h = h0; h < T.heads; h += BATCH * step) {
+      P va[BATCH], vb[BATCH];
 #pragma unroll
-            for (int i = 0; i < N; i += 2) {
-              if (j0 + i < p.plan.rotary) {
-                const float2 cs = table[tok][(j0 + i) >> 1];
-                const float u = f[i], w = f[i + 1];
-                f[i] = fmaf(u, cs.x, -w * cs.y);
-                f[i + 1] = fmaf(w, cs.x, u * cs.y);
-              }
-            }
-          } else {
+      for (int k = 0; k < BATCH; ++k) {
+        const int hh = h + k * step;
+        if (hh < T.heads) {
+          va[k] = *reinterpret_cast<const P *>(x + hh * T.sh + a * V);
+          vb[k] = *reinterpret_cast<const P *>(x + hh * T.sh + b * V);
+        }
+      }
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const int j = j0 + i;
-              if (j < p.plan.rotary) {
-                const bool upper = j >= half;
-                const float2 cs = table[tok][upper ? j - half : j];
-                const float w = simt::load_in(x, upper ? j - half : j + half);
-                f[i] = fmaf(f[i], cs.x, upper ? w * cs.y : -w * cs.y);
-              }
-            }
-          }
-          v.set(f);
+      for (int k = 0; k < BATCH; ++k) {
+        const int hh = h + k * step;
+        if (hh < T.heads) {
+          turned(va[k], vb[k]);
+          *reinterpret_cast<P *>(y + hh * y_head + a * V) = va[k];
+          *reinterpret_cast<P *>(y + hh * y_head + b * V) = vb[k];
         }
       }
     }
-    va.store(y + a * N);
-    vb.store(y + b * N);
   }
 }
 

@@ -1035,19 +1035,31 @@ int run_rope(const void *Q, const void *K, int dtype, const int *positions, int 
   p.sin_sign = inverse ? -1.f : 1.f;
   p.T = T;
   p.tokens = tokens;
-  const long long tiles = (tokens + rope::TILE - 1) / rope::TILE;
-  // A tile's angles are made by every CTA that shares its heads: one CTA a tile where the tiles fill
-  // the SMs, else enough to.
-  const int vec = (int)(16 / elt), rows_a_step = rope::THREADS / (rope::D / vec / 2);
-  const long long steps = (rope::TILE * heads + rows_a_step - 1) / rows_a_step;
-  p.head_groups = (int)std::max<long long>(1, std::min<long long>(steps, 8 * ATTN_SMS / tiles));
-  const bool paired = !interleaved && (rotary_dim / 2) % vec == 0;
-  auto kernel =
-      dtype == TTT_BF16
-          ? (interleaved ? rope::rope_kernel<__nv_bfloat16, rope::INTERLEAVED>
-                         : paired ? rope::rope_kernel<__nv_bfloat16, rope::PAIRED> : rope::rope_kernel<__nv_bfloat16, rope::ANY>)
-          : (interleaved ? rope::rope_kernel<float, rope::INTERLEAVED>
-                         : paired ? rope::rope_kernel<float, rope::PAIRED> : rope::rope_kernel<float, rope::ANY>);
+  // Values of a piece (see rope.cuh).
+  int vec = (int)(16 / elt);
+  while (!interleaved && (rotary_dim / 2) % vec != 0) vec >>= 1;
+  // Tiles of 16 tokens (no more than a CTA has rows) share a CTA's angles best; with fewer than two tiles
+  // an SM smaller ones, so that all SMs have work, and then several CTAs a tile, each with a part of the
+  // heads (and the tile's angles again).
+  const int rows_a_step = rope::THREADS / (rope::D / vec / 2);
+  p.tile = std::min(rope::MOST_TILE, rows_a_step);
+  while (p.tile > 1 && tokens < 2LL * ATTN_SMS * p.tile) p.tile >>= 1;
+  const long long tiles = (tokens + p.tile - 1) / p.tile;
+  const int heads_a_step = rows_a_step / p.tile;
+  const long long steps = (std::max(Hq, Hk) + heads_a_step - 1) / heads_a_step;
+  p.head_groups = (int)std::max<long long>(1, std::min<long long>(steps, 2 * ATTN_SMS / tiles));
+  auto kernel = [&] {
+    if (dtype == TTT_BF16) {
+      using T = __nv_bfloat16;
+      if (interleaved) return rope::rope_kernel<T, 8, true>;
+      return vec == 8 ? rope::rope_kernel<T, 8, false>
+                      : vec == 4 ? rope::rope_kernel<T, 4, false>
+                                 : vec == 2 ? rope::rope_kernel<T, 2, false> : rope::rope_kernel<T, 1, false>;
+    }
+    if (interleaved) return rope::rope_kernel<float, 4, true>;
+    return vec == 4 ? rope::rope_kernel<float, 4, false>
+                    : vec == 2 ? rope::rope_kernel<float, 2, false> : rope::rope_kernel<float, 1, false>;
+  }();
   return launch_attn(kernel, tiles * p.head_groups, rope::THREADS, 0, static_cast<cudaStream_t>(stream), p);
 }
 

@@ -167,7 +167,7 @@ def test_decode_many_units_are_each_their_own():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("rotary", [64, 48, 40, 20, 2, 0])
+@pytest.mark.parametrize("rotary", [64, 48, 40, 20, 14, 2, 0])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("inverse", [False, True])
 def test_rope(dtype, rotary, interleaved, inverse):
