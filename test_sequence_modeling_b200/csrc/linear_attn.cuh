@@ -89,15 +89,15 @@ __device__ __forceinline__ Segment segment_of(const Params &p, int k) {
   return g;
 }
 // The state a segment starts from (NULL: zero).
-__device__ __forceinline__ const float *start_state(const Params &p, const Segment &g) {
+__device__ __forceinline__ const float *start_state(const Params &p, int unit, int slot) {
   if (p.slots_out) return nullptr;
-  if (g.slot >= 0) return p.slots + (long long)g.slot * (D * D);
-  return p.C0 ? p.C0 + (long long)g.unit * (D * D) : nullptr;
+  if (slot >= 0) return p.slots + (long long)slot * (D * D);
+  return p.C0 ? p.C0 + (long long)unit * (D * D) : nullptr;
 }
 // Where the state it ends in goes (NULL: nowhere).
-__device__ __forceinline__ float *end_state(const Params &p, const Segment &g) {
-  if (p.slots_out) return g.last ? nullptr : p.slots_out + (long long)g.slot * (D * D);
-  return p.C_out && g.last ? p.C_out + (long long)g.unit * (D * D) : nullptr;
+__device__ __forceinline__ float *end_state(const Params &p, int unit, int slot, bool last) {
+  if (p.slots_out) return last ? nullptr : p.slots_out + (long long)slot * (D * D);
+  return p.C_out && last ? p.C_out + (long long)unit * (D * D) : nullptr;
 }
 
 __device__ __forceinline__ float decay_pow(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(THREADS, 2) attn_kernel(const Params p) {
   const bool has_state = STATE_ONLY || half == 0;
   float C[ROWS][8];
   if (has_state) {
-    const float *C0 = start_state(p, sg);
+    const float *C0 = start_state(p, sg.unit, sg.slot);
 #pragma unroll
     for (int i = 0; i < ROWS; ++i)
 #pragma unroll
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 2) attn_kernel(const Params p) {
       store_out(out + (long long)r * D + 4 * (tid & 15), make_float4(0.f, 0.f, 0.f, 0.f));
   }
   if (has_state) {
-    if (float *Co = end_state(p, sg)) state_to(Co, D);
+    if (float *Co = end_state(p, sg.unit, sg.slot, sg.last)) state_to(Co, D);
   }
 }
 

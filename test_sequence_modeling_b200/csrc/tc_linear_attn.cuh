@@ -9,6 +9,7 @@
 // segment without a stop); the roles run apart and meet at mbarriers:
 //   warp 0        TMA: x, y, w tiles of a chunk, two slots each, refilled one by one
 //   warp 1        issues every product: w^T y', x C, the next chunk's x y^T, P w
+//   warp 3        says ahead which segments there are, with their powers of gamma
 //   warps 4-11    P: row t of 128 columns out of tensor memory (two warps a row), masked and
 //                 decayed, back as the bf16 A operand of P w
 //   warps 12-15   y' = e h_s y_s as three bf16 tiles, two buffers
@@ -65,12 +66,22 @@ constexpr uint32_t OFF_YS = 6 * TILE;            // y' in three parts
 constexpr uint32_t OFF_C = OFF_YS + 6 * TILE;    // C^T [64][64] bf16
 constexpr uint32_t C_BYTES = D * D * 2;
 constexpr uint32_t OFF_OUT = OFF_C + 2 * C_BYTES;  // output tile (one)
-constexpr uint32_t OFF_PA = OFF_OUT + TILE;        // a gamma^0 .. a gamma^127
-constexpr uint32_t OFF_CT = OFF_PA + CHUNK * 4;    // gamma^31 .. gamma^0 (reverse: gamma^0 ..)
-constexpr uint32_t OFF_BAR = OFF_CT + 32 * 4;
-constexpr uint32_t OFF_TSLOT = OFF_BAR + 32 * 8;
+constexpr uint32_t OFF_SEG = OFF_OUT + TILE;       // 2 segments said ahead
+struct Said {
+  int valid;           // 0: there are no more
+  int unit, t_lo, rows, n, nchunks;  // its place, its rows and tokens, their chunks
+  int last, slot;      // as in lattn::Segment
+  int hand_to;         // the slot of the state that it hands on, or -1
+  float log_decay;
+  int pad[2];
+  float ct[32];        // gamma^31 .. gamma^0 (reverse: gamma^0 ..)
+  float pw[CHUNK + 4]; // gamma^0 .. gamma^128
+};
+constexpr uint32_t OFF_BAR = OFF_SEG + 2 * sizeof(Said);
+constexpr uint32_t OFF_TSLOT = OFF_BAR + 28 * 8;
 constexpr uint32_t OFF_ABORT = OFF_TSLOT + 4;
-constexpr uint32_t OFF_NUMBER = OFF_ABORT + 4;
+constexpr uint32_t OFF_TOTAL = OFF_ABORT + 4;
+constexpr uint32_t OFF_NUMBER = OFF_TOTAL + 4;
 constexpr uint32_t SMEM_USED = OFF_NUMBER + 4;
 constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024, "one CTA's shared memory");
@@ -85,11 +96,12 @@ enum {
   FX = 0, FY = 2, FW = 4,        // a slot's tile is loaded
   EX = 6, EY = 8, EW = 10,       // and read
   PFULL = 12, PREADY = 13, YREADY = 14, CREADY = 16, MFULL = 17, OFULL = 19, OFREE = 20, NEVER = 21, DRAIN = 22,
-  NUM_BARS = 23
+  SAID = 23, HEARD = 25, SUM = 27,  // a segment is said, and done with; the number of chunks is known
+  NUM_BARS = 28
 };
 constexpr long long WAIT_LIMIT = 1ll << 32;            // SM cycles, ~2 s
 constexpr long long INJECTED_WAIT_LIMIT = 1ll << 20;
-constexpr uint32_t NB_OUT = 1, NB_P = 2;               // named barriers of the output and the P warps
+constexpr int OUT_ROWS = 32;                           // rows of an output store: one warp's
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -212,7 +224,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool warps4 = i == YREADY || i == YREADY + 1 || i == CREADY || i == OFREE;
       // A y slot is read by the four warps that decay it and by the product P.
       const bool y_slot = i == EY || i == EY + 1;
-      mbar_init(&bars[i], i == PREADY ? 8 : y_slot ? (STATE_ONLY ? 4 : 5) : warps4 ? 4 : 1);
+      const bool heard = i == HEARD || i == HEARD + 1;  // by the warps of loads, P, y', state and outputs
+      mbar_init(&bars[i], heard ? (STATE_ONLY ? 9 : 21) : i == PREADY ? 8 : y_slot ? (STATE_ONLY ? 4 : 5) : warps4 ? 4 : 1);
     }
     *abort = 0;
     fence_mbarrier_init();
@@ -234,65 +247,31 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after_sync();
   const uint32_t tb = *tslot;  // all columns are this CTA's: the base is 0, which the roles take as a constant
 
-  // This CTA's segments, one after the other, their tokens and chunks.
   const int cta = *number;
-  int unit_a = 0, step_a = 0, unit_b = 0, step_b = 0;  // the ends of its range
-  if (shared.steps) {
-    const long long total = (long long)shared.units * shared.steps;
-    const long long a = total * cta / gridDim.x, b = total * (cta + 1) / gridDim.x;
-    unit_a = (int)(a / shared.steps), step_a = (int)(a - (long long)unit_a * shared.steps);
-    unit_b = (int)(b / shared.steps), step_b = (int)(b - (long long)unit_b * shared.steps);
-  }
-  struct Segment : lattn::Segment {
-    int n, nchunks;
-    int hand_to;  // the slot of the state that it hands on, or -1
+  auto chunk_start = [](int nchunks, int c) { return (REVERSE ? nchunks - 1 - c : c) * CHUNK; };
+  Said *segments = reinterpret_cast<Said *>(sm + OFF_SEG);
+  // Segment k, as warp 3 says it; false: there is none, or a wait ran out.
+  auto hear = [&](int k, bool &ok) {
+    if (ok) ok = wait_warp(&bars[SAID + (k & 1)], (uint32_t)(k >> 1) & 1u, abort);
+    return ok && segments[k & 1].valid;
   };
-  auto segment = [&](int idx, Segment &g) {
-    g.hand_to = -1;
-    if (!shared.steps) {
-      const int k = cta + idx * (int)gridDim.x;
-      if (k >= p.segments) return false;
-      static_cast<lattn::Segment &>(g) = lattn::segment_of<REVERSE>(p, p.first_segment + k);
-    } else {
-      const int whole0 = step_a ? unit_a + 1 : unit_a;
-      const int k = idx - (step_b ? 1 : 0) + whole0;
-      int lo = 0, hi = shared.steps;
-      if (step_b && idx == 0) {
-        g.unit = unit_b;
-        hi = step_b;
-        g.hand_to = cta;
-      } else if (k < unit_b) {
-        g.unit = k;
-      } else if (k == unit_b && step_a) {
-        g.unit = unit_a;
-        lo = step_a;
-      } else {
-        return false;
-      }
-      g.t_lo = (REVERSE ? shared.steps - hi : lo) * CHUNK;
-      g.rows = min((REVERSE ? shared.steps - lo : hi) * CHUNK, p.T) - g.t_lo;
-      g.last = hi == shared.steps;
-      g.slot = lo ? cta - 1 : -1;
-    }
-    g.n = min(max(lattn::sequence_length(p.lengths, g.unit / p.H, p.T) - g.t_lo, 0), g.rows);
-    if (STATE_ONLY && g.last) g.n = 0;  // no segment follows it: its own state has no reader
-    g.nchunks = (g.n + CHUNK - 1) / CHUNK;
-    return true;
+  auto heard = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[HEARD + (k & 1)]);
   };
-  auto chunk_start = [](const Segment &g, int c) { return (REVERSE ? g.nchunks - 1 - c : c) * CHUNK; };
-  auto log_decay = [&](const Segment &g) { return p.log_decay[g.unit % p.H]; };
 
   bool ok = true;
   if (inject_timeout) ok = wait(&bars[NEVER], 0, abort, INJECTED_WAIT_LIMIT);
 
   if (warp == 0) {
     // ---- loads -------------------------------------------------------------------
-    if (lane == 0) {
-      int i = 0;
-      Segment g;
-      for (int k = 0; ok && segment(k, g); ++k) {
-        for (int c = 0; ok && c < g.nchunks; ++c, ++i) {
-          const int slot = i & 1, t0 = g.t_lo + chunk_start(g, c);
+    int i = 0;
+    for (int k = 0; hear(k, ok); ++k) {
+      const Said &g = segments[k & 1];
+      const int nchunks = g.nchunks;
+      if (lane == 0) {
+        for (int c = 0; ok && c < nchunks; ++c, ++i) {
+          const int slot = i & 1, t0 = g.t_lo + chunk_start(nchunks, c);
           const uint32_t par = (uint32_t)(i / 2 - 1) & 1u;
           auto load = [&](int full, int empty, uint32_t off, const CUtensorMap *map) {
             if (i > 1 && !wait(&bars[empty + slot], par, abort)) return false;
@@ -304,18 +283,91 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = load(FY, EY, OFF_Y, &tmY) && (STATE_ONLY || load(FX, EX, OFF_X, &tmX)) && load(FW, EW, OFF_W, &tmW);
         }
       }
-      // A CTA that gave up lets its loads in flight land: the tiles of the last chunks, of which the
-      // very last may lack some (a wait for those runs out at once: they count as never armed).
-      if (*abort) {
-        for (int j = max(0, i - 3); j < i; ++j) {
-          const uint32_t par = (uint32_t)(j / 2) & 1u;
-          mbar_wait(&bars[FY + (j & 1)], par, INJECTED_WAIT_LIMIT);
-          if (!STATE_ONLY) mbar_wait(&bars[FX + (j & 1)], par, INJECTED_WAIT_LIMIT);
-          mbar_wait(&bars[FW + (j & 1)], par, INJECTED_WAIT_LIMIT);
-        }
+      ok = __all_sync(0xffffffffu, ok);
+      heard(k);
+    }
+    // A CTA that gave up lets its loads in flight land: the tiles of the last chunks, of which the
+    // very last may lack some (a wait for those runs out soon: they count as never armed).
+    if (lane == 0 && *abort) {
+      for (int j = max(0, i - 3); j < i; ++j) {
+        const uint32_t par = (uint32_t)(j / 2) & 1u;
+        mbar_wait(&bars[FY + (j & 1)], par, INJECTED_WAIT_LIMIT);
+        if (!STATE_ONLY) mbar_wait(&bars[FX + (j & 1)], par, INJECTED_WAIT_LIMIT);
+        mbar_wait(&bars[FW + (j & 1)], par, INJECTED_WAIT_LIMIT);
       }
     }
     __syncwarp();
+  } else if (warp == 3) {
+    // ---- segments -----------------------------------------------------------------------
+    // One after the other, a segment ahead of the warps that take them: what leads from one segment to
+    // the next is long, rarely run code, which would stand in the way of five roles.
+    int unit_a = 0, step_a = 0, unit_b = 0, step_b = 0;  // the ends of a shared range
+    if (shared.steps) {
+      const long long all = (long long)shared.units * shared.steps;
+      const long long a = all * cta / gridDim.x, b = all * (cta + 1) / gridDim.x;
+      unit_a = (int)(a / shared.steps), step_a = (int)(a - (long long)unit_a * shared.steps);
+      unit_b = (int)(b / shared.steps), step_b = (int)(b - (long long)unit_b * shared.steps);
+    }
+    auto segment = [&](int idx, Said &g) {
+      g.hand_to = -1;
+      if (!shared.steps) {
+        const int k = cta + idx * (int)gridDim.x;
+        if (k >= p.segments) return false;
+        const lattn::Segment o = lattn::segment_of<REVERSE>(p, p.first_segment + k);
+        g.unit = o.unit, g.t_lo = o.t_lo, g.rows = o.rows, g.last = o.last, g.slot = o.slot;
+      } else {
+        const int whole0 = step_a ? unit_a + 1 : unit_a;
+        const int k = idx - (step_b ? 1 : 0) + whole0;
+        int lo = 0, hi = shared.steps;
+        if (step_b && idx == 0) {
+          g.unit = unit_b;
+          hi = step_b;
+          g.hand_to = cta;
+        } else if (k < unit_b) {
+          g.unit = k;
+        } else if (k == unit_b && step_a) {
+          g.unit = unit_a;
+          lo = step_a;
+        } else {
+          return false;
+        }
+        g.t_lo = (REVERSE ? shared.steps - hi : lo) * CHUNK;
+        g.rows = min((REVERSE ? shared.steps - lo : hi) * CHUNK, p.T) - g.t_lo;
+        g.last = hi == shared.steps;
+        g.slot = lo ? cta - 1 : -1;
+      }
+      g.n = min(max(lattn::sequence_length(p.lengths, g.unit / p.H, p.T) - g.t_lo, 0), g.rows);
+      if (STATE_ONLY && g.last) g.n = 0;  // no segment follows it: its own state has no reader
+      g.nchunks = (g.n + CHUNK - 1) / CHUNK;
+      return true;
+    };
+    Said g;
+    int total = 0;
+    for (int k = 0; segment(k, g); ++k) total += g.nchunks;
+    if (lane == 0) {
+      *reinterpret_cast<int *>(sm + OFF_TOTAL) = total;
+      mbar_arrive(&bars[SUM]);
+    }
+    for (int k = 0; ok; ++k) {
+      if (k > 1 && !(ok = wait_warp(&bars[HEARD + (k & 1)], (uint32_t)(k / 2 - 1) & 1u, abort))) break;
+      Said &to = segments[k & 1];
+      const bool valid = segment(k, g);
+      if (valid) {
+        g.log_decay = p.log_decay[g.unit % p.H];
+        for (int n = lane; n <= CHUNK; n += 32) to.pw[n] = decay_pow(g.log_decay, n);
+        to.ct[lane] = decay_pow(g.log_decay, REVERSE ? lane : 31 - lane);
+      }
+      if (lane == 0) {
+        to.valid = valid;
+        if (valid) {
+          to.unit = g.unit, to.t_lo = g.t_lo, to.rows = g.rows, to.n = g.n, to.nchunks = g.nchunks;
+          to.last = g.last, to.slot = g.slot, to.hand_to = g.hand_to, to.log_decay = g.log_decay;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[SAID + (k & 1)]);
+      if (!valid) break;
+    }
   } else if (warp == 1) {
     // ---- products (the whole warp, converged; one lane elected to issue).  They do not depend on
     // where a segment ends. -----------------------------------------------------------------
@@ -323,9 +375,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr uint32_t ID_XC = idesc_bf16_f32(128, 64, false, false, false);
     constexpr uint32_t ID_PW = idesc_bf16_f32(128, 64, false, true, false);
     constexpr uint32_t ID_M = idesc_bf16_f32(64, 192, true, true, false);
-    int total = 0;
-    Segment g;
-    for (int k = 0; segment(k, g); ++k) total += g.nchunks;
+    if (ok) ok = wait_warp(&bars[SUM], 0, abort);
+    const int total = ok ? *reinterpret_cast<const int *>(sm + OFF_TOTAL) : 0;
     auto scores = [&](int i) {  // P of chunk i, once its tiles are in
       const uint32_t slot = i & 1, par = (uint32_t)(i >> 1) & 1u;
       if (!wait_warp(&bars[FX + slot], par, abort) || !wait_warp(&bars[FY + slot], par, abort)) return false;
@@ -379,23 +430,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---- P: mask and decay, to bf16 ------------------------------------------------------
     // Row t = 32 w4 + lane, blocks 2 half and 2 half + 1 of 32 columns.  Off the diagonal block the
     // power of gamma is the product of one of the row's and one of the column's (ct), both at most 1.
-    // (These warps, like the outputs', meet at a named barrier, so none leaves its loops alone: after
-    // a wait that ran out they run on whatever the tensor memory holds.)
-    float *pa = reinterpret_cast<float *>(sm + OFF_PA), *ct = reinterpret_cast<float *>(sm + OFF_CT);
-    const int half = (warp - 4) >> 2, ptid = tid - 128;
+    const int half = (warp - 4) >> 2;
     const uint32_t row = tmem_addr(0, 32 * w4, T_P), dst = tmem_addr(0, 32 * w4, T_PB);
+    const float2 a2 = make_float2(p.a, p.a);
     int i = 0;
-    Segment g;
-    for (int k = 0; segment(k, g); ++k) {
-      if (g.nchunks == 0) continue;
-      const float ld = log_decay(g);
-      named_barrier_sync(NB_P, 256);  // the last segment's tables are read
-      if (ptid < CHUNK) pa[ptid] = p.a * decay_pow(ld, ptid);
-      else if (ptid < CHUNK + 32) ct[ptid - CHUNK] = decay_pow(ld, REVERSE ? ptid - CHUNK : CHUNK + 31 - ptid);
-      named_barrier_sync(NB_P, 256);
-      for (int c = 0; c < g.nchunks; ++c, ++i) {
-        const int n = min(CHUNK, g.n - chunk_start(g, c));
-        if (ok) ok = wait_warp(&bars[PFULL], (uint32_t)i & 1u, abort);
+    for (int k = 0; hear(k, ok); ++k) {
+      const Said &g = segments[k & 1];
+      const int nchunks = g.nchunks, ntok = g.n;
+      const float *pw = g.pw, *ct = g.ct;
+      for (int c = 0; c < nchunks; ++c, ++i) {
+        const int n = min(CHUNK, ntok - chunk_start(nchunks, c));
+        if (!(ok = wait_warp(&bars[PFULL], (uint32_t)i & 1u, abort))) break;
         tc_fence_after_sync();
 #pragma unroll 1
         for (int j = 2 * half; j < 2 * half + 2; ++j) {
@@ -409,7 +454,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_ld_32x32b_x32(row + 32 * j, r);
             const int end = REVERSE ? n - 32 * j : 32;  // columns that hold tokens (forward: s <= t decides)
             if (d == 0 || end < 32) {
-              const float *f = pa + (REVERSE ? 32 * d - lane : 32 * d + lane);
+              const float *f = pw + (REVERSE ? 32 * d - lane : 32 * d + lane);
               const int most = REVERSE ? end : 32 * d + lane + 1, least = REVERSE ? lane - 32 * d : 0;
               tmem_wait_ld();
               loaded(r);
@@ -422,10 +467,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                   const bool in = s < most && s >= least;
                   v[h] = in ? __uint_as_float(r[s]) * f[REVERSE ? s : -s] : 0.f;
                 }
-                pk[e] = pack_bf16x2(v[0], v[1]);
+                const float2 u = __fmul2_rn(a2, make_float2(v[0], v[1]));
+                pk[e] = pack_bf16x2(u.x, u.y);
               }
             } else {
-              const float b = pa[REVERSE ? 32 * d - lane : lane + 32 * d - 31];
+              const float b = p.a * pw[REVERSE ? 32 * d - lane : lane + 32 * d - 31];
               const float2 b2 = make_float2(b, b);
               tmem_wait_ld();
               loaded(r);
@@ -442,14 +488,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
           // The last chunk's P w has read what this overwrites.
-          if (ok && i > 0 && j == 2 * half) ok = wait_warp(&bars[OFULL], (uint32_t)(i - 1) & 1u, abort);
+          if (i > 0 && j == 2 * half && !(ok = wait_warp(&bars[OFULL], (uint32_t)(i - 1) & 1u, abort))) break;
           tmem_st_32x32b_x16(dst + 16 * j, pk);
         }
+        if (!ok) break;
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[PREADY]);
       }
+      heard(k);
     }
   } else if (warp >= 12 && warp < 16) {
     // ---- y' (zeros past the end), and zeros over w's rows past the end: what lies there is any
@@ -457,12 +505,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int s = 32 * w4 + lane;
     const uint32_t row = sw128_offset(s, 0);  // piece q of the row is at row ^ (16 q)
     int i = 0;
-    Segment g;
-    for (int k = 0; ok && segment(k, g); ++k) {
-      const float ld = log_decay(g);
-      const float h_full = p.e * decay_pow(ld, REVERSE ? s + 1 : CHUNK - 1 - s);
-      for (int c = 0; ok && c < g.nchunks; ++c, ++i) {
-        const int n = min(CHUNK, g.n - chunk_start(g, c));
+    for (int k = 0; hear(k, ok); ++k) {
+      const Said &g = segments[k & 1];
+      const int nchunks = g.nchunks, ntok = g.n;
+      const float h_full = p.e * g.pw[REVERSE ? s + 1 : CHUNK - 1 - s];
+      for (int c = 0; ok && c < nchunks; ++c, ++i) {
+        const int n = min(CHUNK, ntok - chunk_start(nchunks, c));
         const uint32_t slot = i & 1, par2 = (uint32_t)(i >> 1) & 1u;
         uint8_t *ty = sm + OFF_Y + slot * TILE;
         uint8_t *ys = sm + OFF_YS + slot * (3 * TILE);
@@ -471,7 +519,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (i > 1 && !(ok = wait_warp(&bars[MFULL + slot], par2 ^ 1u, abort))) break;
         float h1 = h_full;
         if (n < CHUNK) {
-          if (!REVERSE) h1 = p.e * decay_pow(ld, max(n - 1 - s, 0));
+          if (!REVERSE) h1 = p.e * g.pw[max(n - 1 - s, 0)];
           if (!(ok = wait_warp(&bars[FW + slot], par2, abort))) break;
           if (s >= n) {
 #pragma unroll 1
@@ -509,6 +557,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           mbar_arrive(&bars[YREADY + slot]);
         }
       }
+      heard(k);
     }
   } else if (warp >= 16 && warp < 20) {
     // ---- state ----------------------------------------------------------------------
@@ -517,14 +566,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     // C[4 j + {2, 3}].
     const int row = 16 * w4 + (lane >> 2), col = 2 * (lane & 3);
     int i = 0;
-    Segment g;
-    for (int k = 0; ok && segment(k, g); ++k) {
-      const float ld = log_decay(g);
-      const float d_full = decay_pow(ld, CHUNK);
+    for (int k = 0; hear(k, ok); ++k) {
+      const Said &g = segments[k & 1];
+      const int nchunks = g.nchunks, ntok = g.n;
       float C[32];
       {
         if (shared.steps && g.slot >= 0 && !(ok = wait_handed(shared.ticket + 1 + g.slot, abort))) break;
-        const float *C0 = lattn::start_state(p, g);
+        const float *C0 = lattn::start_state(p, g.unit, g.slot);
         const bool as_is = p.transposed || (shared.steps && g.slot >= 0);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
@@ -532,7 +580,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           C[e] = C0 ? __ldcg(C0 + (as_is ? r * D + cc : cc * D + r)) : 0.f;
         }
       }
-      for (int c = 0; c < g.nchunks; ++c, ++i) {
+      for (int c = 0; c < nchunks; ++c, ++i) {
         // The operand of x C, in the buffer whose last reader, x C two chunks ago, was issued before
         // the last chunk's w^T y', whose end these warps have seen.
         if (!STATE_ONLY) {
@@ -546,8 +594,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[CREADY]);
-        const int n = min(CHUNK, g.n - chunk_start(g, c));
-        const float dn = n < CHUNK ? decay_pow(ld, n) : d_full;
+        const int n = min(CHUNK, ntok - chunk_start(nchunks, c));
+        const float dn = g.pw[n];
         if (!(ok = wait_warp(&bars[MFULL + (i & 1)], (uint32_t)(i >> 1) & 1u, abort))) break;
         tc_fence_after_sync();
 #pragma unroll
@@ -574,28 +622,27 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) Co[(row + 8 * ((e >> 1) & 1)) * D + 8 * (e >> 2) + col + (e & 1)] = C[e];
         hand_on(shared.ticket + 1 + g.hand_to);
-      } else if (float *Co = lattn::end_state(p, g)) {
+      } else if (float *Co = lattn::end_state(p, g.unit, g.slot, g.last)) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) Co[(8 * (e >> 2) + col + (e & 1)) * D + row + 8 * ((e >> 1) & 1)] = C[e];
       }
+      heard(k);
     }
   } else if (!STATE_ONLY && warp >= 20) {
-    // ---- outputs --------------------------------------------------------------------
+    // ---- outputs: each warp its own 32 rows ---------------------------------------------
     const int t = 32 * w4 + lane;
     int i = 0;
-    Segment g;
-    for (int k = 0; segment(k, g); ++k) {
-      const float ld = log_decay(g);
-      const float f_full = p.c * decay_pow(ld, REVERSE ? CHUNK - 1 - t : t + 1);
-      for (int c = 0; c < g.nchunks; ++c, ++i) {
-        const int c0 = chunk_start(g, c), n = min(CHUNK, g.n - c0);
-        const float f1 = REVERSE && n < CHUNK ? p.c * decay_pow(ld, max(n - 1 - t, 0)) : f_full;
+    for (int k = 0; hear(k, ok); ++k) {
+      const Said &g = segments[k & 1];
+      const int nchunks = g.nchunks, ntok = g.n;
+      for (int c = 0; c < nchunks; ++c, ++i) {
+        const int c0 = chunk_start(nchunks, c), n = min(CHUNK, ntok - c0);
+        const float f1 = p.c * g.pw[REVERSE ? max(n - 1 - t, 0) : t + 1];
         const float2 f = make_float2(f1, f1);
-        if (ok) ok = wait_warp(&bars[OFULL], (uint32_t)i & 1u, abort);
+        if (!(ok = wait_warp(&bars[OFULL], (uint32_t)i & 1u, abort))) break;
         tc_fence_after_sync();
-        // The tile is free once the last store has read it.
-        if (warp == 20 && lane == 0) tma_store_wait_read();
-        named_barrier_sync(NB_OUT, 128);
+        if (lane == 0) tma_store_wait_read();  // the warp's last store has read the tile
+        __syncwarp();
 #pragma unroll 1
         for (int h = 0; h < 4; ++h) {
           uint32_t xc[16], pv[16], o[8];
@@ -621,17 +668,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before_sync();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[OFREE]);
-        named_barrier_sync(NB_OUT, 128);
-        if (warp == 20 && lane == 0) tma_store_3d(&tmOut, sm + OFF_OUT, 0, g.t_lo + c0, g.unit);
+        if (lane == 0) {
+          mbar_arrive(&bars[OFREE]);
+          const int t0 = g.t_lo + c0 + 32 * w4;
+          if (t0 < p.T) tma_store_3d(&tmOut, sm + OFF_OUT + 32 * w4 * 128, 0, t0, g.unit);
+        }
       }
       // Rows of chunks wholly behind the end (those of the last chunk are in its tile).
       __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + ((long long)g.unit * p.T + g.t_lo) * D;
-      const int x0 = min(g.nchunks * CHUNK, g.rows) * (D / 8), x1 = g.rows * (D / 8);
+      const int x0 = min(nchunks * CHUNK, g.rows) * (D / 8), x1 = g.rows * (D / 8);
       for (int x = x0 + (tid & 127); x < x1; x += 128)
         reinterpret_cast<uint4 *>(out)[x] = make_uint4(0u, 0u, 0u, 0u);
+      heard(k);
     }
-    if (warp == 20 && lane == 0) tma_store_wait_read();
+    if (lane == 0) tma_store_wait_read();
     __syncwarp();
   }
   tc_fence_before_sync();

@@ -817,7 +817,7 @@ int launch_attn_tc(long long units, const lattn::Params &p, int steps, int *tick
   CUtensorMap mx, my, mw, mo;
   if (!make_qkv_map(&my, p.Y, p.T, units, tclattn::CHUNK) || !make_qkv_map(&mw, p.W, p.T, units, tclattn::CHUNK) ||
       !make_qkv_map(&mx, STATE_ONLY ? p.Y : p.X, p.T, units, tclattn::CHUNK) ||
-      !make_qkv_map(&mo, STATE_ONLY ? p.Y : p.out, p.T, units, tclattn::CHUNK))
+      !make_qkv_map(&mo, STATE_ONLY ? p.Y : p.out, p.T, units, tclattn::OUT_ROWS))
     return TTT_ERR_CUDA;
   auto kernel = tclattn::attn_tc_kernel<REVERSE, STATE_ONLY>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tclattn::SMEM_BYTES) != cudaSuccess)
