@@ -44,11 +44,14 @@ constexpr int THREADS = 128;
 constexpr int STEP_THREADS = 256;  // of the single-token step
 constexpr int LD = D + 4;  // padded row stride: 8 rows' float4 at one column hit 8 distinct bank groups
 
-// How the units' sequences are dealt out to segments: units below `whole` are one segment each, the others are
-// cut into nseg segments of seg_len tokens (whole chunks of every kernel).  Segment k of the grid:
+// How the units' sequences are dealt out to segments: units below `whole` are one segment each, the others
+// are cut into nseg segments of seg_len tokens (whole chunks of every kernel).  For states alone only the
+// cut units count, without their last segments, which no segment follows.
 struct Cut {
   int whole, nseg, seg_len;
-  __host__ __device__ int segments(int units) const { return whole + (units - whole) * nseg; }
+  __host__ __device__ int segments(int units, bool state_only) const {
+    return state_only ? (units - whole) * (nseg - 1) : whole + (units - whole) * nseg;
+  }
 };
 struct Segment {
   int unit;
@@ -71,21 +74,29 @@ struct Params {
                            // units' segments leave by themselves (the last one's has no reader)
   int H, T;
   Cut cut;
-  int first_segment, segments;  // this launch's
+  int segments;            // this launch's
 };
 
-template <bool REVERSE>
-__device__ __forceinline__ Segment segment_of(const Params &p, int k) {
+// The passes of one launch: the forward's one, or the three of a backward (the first one forward, the
+// others in reverse; or one of each for states alone), which have no part in one another.
+constexpr int MOST_PASSES = 3;
+struct Passes {
+  Params p[MOST_PASSES];
+};
+
+// Segment k of a launch; its slot, for states alone, is that of the state that it leaves.
+template <bool STATE_ONLY>
+__device__ __forceinline__ Segment segment_of(const Params &p, int k, bool reverse) {
   Segment g;
-  const int rest = k - p.cut.whole;
+  const int rest = STATE_ONLY ? k : k - p.cut.whole, n = STATE_ONLY ? p.cut.nseg - 1 : p.cut.nseg;
   const bool cut = rest >= 0;
-  const int q = cut ? rest / p.cut.nseg : 0, seg = cut ? rest - q * p.cut.nseg : 0;
-  const int n = cut ? p.cut.nseg : 1, len = cut ? p.cut.seg_len : p.T;
+  const int q = cut ? rest / n : 0, seg = cut ? rest - q * n + (STATE_ONLY && reverse) : 0;
+  const int len = cut ? p.cut.seg_len : p.T;
   g.unit = cut ? p.cut.whole + q : k;
   g.t_lo = seg * len;
   g.rows = min(len, p.T - g.t_lo);
-  g.last = REVERSE ? seg == 0 : seg == n - 1;
-  g.slot = cut ? rest : -1;
+  g.last = !STATE_ONLY && (!cut || seg == (reverse ? 0 : p.cut.nseg - 1));
+  g.slot = cut ? q * p.cut.nseg + seg : -1;
   return g;
 }
 // The state a segment starts from (NULL: zero).
@@ -96,7 +107,7 @@ __device__ __forceinline__ const float *start_state(const Params &p, int unit, i
 }
 // Where the state it ends in goes (NULL: nowhere).
 __device__ __forceinline__ float *end_state(const Params &p, int unit, int slot, bool last) {
-  if (p.slots_out) return last ? nullptr : p.slots_out + (long long)slot * (D * D);
+  if (p.slots_out) return p.slots_out + (long long)slot * (D * D);
   return p.C_out && last ? p.C_out + (long long)unit * (D * D) : nullptr;
 }
 
@@ -164,7 +175,7 @@ constexpr size_t SMEM_BYTES = sizeof(float) * (size_t)(5 * CHUNK * LD + 2 * CHUN
 // 4 x 4 tiles and 256 threads the operands' reads from shared memory took twice the arithmetic's time:
 // forward B6 H8 T1999 145 us, against 121 now, of which the arithmetic is about half.
 template <typename InT, bool REVERSE, bool STATE_ONLY>
-__global__ void __launch_bounds__(THREADS, 2) attn_kernel(const Params p) {
+__device__ __forceinline__ void attn_segment(const Params &p, int segment) {
   extern __shared__ __align__(16) float sm[];
   float *Xs = sm;                // [CHUNK][LD]
   float *Ys = Xs + CHUNK * LD;
@@ -173,8 +184,7 @@ __global__ void __launch_bounds__(THREADS, 2) attn_kernel(const Params p) {
   float *Cs = Ms + CHUNK * LD;   // the carried state
   float *pw = Cs + D * LD;       // gamma^0 .. gamma^CHUNK
   const int tid = threadIdx.x, half = tid >> 6, tx = tid & 7, ty = (tid >> 3) & 7;
-  const Segment sg = segment_of<REVERSE>(p, p.first_segment + blockIdx.x);
-  if (STATE_ONLY && sg.last) return;
+  const Segment sg = segment_of<STATE_ONLY>(p, segment, REVERSE);
   const float g = p.log_decay[sg.unit % p.H];
   const int len = sequence_length(p.lengths, sg.unit / p.H, p.T);
   const int n_seg = min(max(len - sg.t_lo, 0), sg.rows);  // its tokens
@@ -328,32 +338,44 @@ __global__ void __launch_bounds__(THREADS, 2) attn_kernel(const Params p) {
   }
 }
 
+template <typename InT, bool STATE_ONLY>
+__global__ void __launch_bounds__(THREADS, 2) attn_kernel(const __grid_constant__ Passes ps) {
+  int k = blockIdx.x;
+  if (k < ps.p[0].segments) return attn_segment<InT, false, STATE_ONLY>(ps.p[0], k);
+  k -= ps.p[0].segments;
+  const int which = k < ps.p[1].segments ? 1 : 2;
+  attn_segment<InT, true, STATE_ONLY>(ps.p[which], which == 1 ? k : k - ps.p[1].segments);
+}
+
 // The states at the segments' starts of the cut units, in place: slot i of a unit holds the state that
 // its segment alone leaves (M_i) and gets the state that it starts from,
 //   C_0 = C0,  C_{i+1} = gamma^(n_i) C_i + M_i     (reverse: from the last segment down).
 // Reads and writes nseg x 16 KB a unit once: bound by memory, and small beside the tokens.
 struct ScanParams {
-  float *slots;  // [cut units][nseg][D][D]
-  const float *C0;
+  float *slots[2];  // [cut units][nseg][D][D] of the forward and the reverse pass
+  const float *C0[2];
   const float *log_decay;
   const int *lengths;
   int H, T;
   Cut cut;
+  int blocks;       // of one pass
 };
 
 constexpr int SCAN_THREADS = 256;  // 4 values a thread: 4 CTAs a unit
 
-template <bool REVERSE>
 __global__ void __launch_bounds__(SCAN_THREADS) scan_kernel(const ScanParams p) {
-  const int q = blockIdx.x >> 2, unit = p.cut.whole + q;
-  const int at = ((blockIdx.x & 3) * SCAN_THREADS + threadIdx.x) * 4;
+  const bool reverse = (int)blockIdx.x >= p.blocks;
+  const int block = reverse ? blockIdx.x - p.blocks : blockIdx.x;
+  const int q = block >> 2, unit = p.cut.whole + q;
+  const int at = ((block & 3) * SCAN_THREADS + threadIdx.x) * 4;
   const float g = p.log_decay[unit % p.H];
   const int len = sequence_length(p.lengths, unit / p.H, p.T);
   float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.C0) c = *reinterpret_cast<const float4 *>(p.C0 + (long long)unit * (D * D) + at);
-  float *slots = p.slots + (long long)q * p.cut.nseg * (D * D) + at;
+  const float *C0 = p.C0[reverse];
+  if (C0) c = *reinterpret_cast<const float4 *>(C0 + (long long)unit * (D * D) + at);
+  float *slots = p.slots[reverse] + (long long)q * p.cut.nseg * (D * D) + at;
   auto slot = [&](int k) {
-    return reinterpret_cast<float4 *>(slots + (long long)(REVERSE ? p.cut.nseg - 1 - k : k) * (D * D));
+    return reinterpret_cast<float4 *>(slots + (long long)(reverse ? p.cut.nseg - 1 - k : k) * (D * D));
   };
   // In batches, whose loads do not wait for one another.
   constexpr int BATCH = 8;
@@ -367,7 +389,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) scan_kernel(const ScanParams p) 
       const int k = k0 + j;
       if (k < p.cut.nseg) *slot(k) = c;
       if (k + 1 < p.cut.nseg) {
-        const int t_lo = (REVERSE ? p.cut.nseg - 1 - k : k) * p.cut.seg_len;
+        const int t_lo = (reverse ? p.cut.nseg - 1 - k : k) * p.cut.seg_len;
         const float dn = decay_pow(g, min(max(len - t_lo, 0), min(p.cut.seg_len, p.T - t_lo)));
         c = make_float4(fmaf(dn, c.x, m[j].x), fmaf(dn, c.y, m[j].y), fmaf(dn, c.z, m[j].z), fmaf(dn, c.w, m[j].w));
       }

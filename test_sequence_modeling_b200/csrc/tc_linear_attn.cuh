@@ -69,13 +69,17 @@ constexpr uint32_t OFF_OUT = OFF_C + 2 * C_BYTES;  // output tile (one)
 constexpr uint32_t OFF_SEG = OFF_OUT + TILE;       // 2 segments said ahead
 struct Said {
   int valid;           // 0: there are no more
+  int pass, reverse;
   int unit, t_lo, rows, n, nchunks;  // its place, its rows and tokens, their chunks
   int last, slot;      // as in lattn::Segment
   int hand_to;         // the slot of the state that it hands on, or -1
-  float log_decay;
-  int pad[2];
-  float ct[32];        // gamma^31 .. gamma^0 (reverse: gamma^0 ..)
-  float pw[CHUNK + 4]; // gamma^0 .. gamma^128
+  float full;          // gamma^128
+  // Powers of gamma, laid out so that either way their users count down in the columns:
+  float ct[32];        // gamma^31 .. gamma^0; reverse: gamma^0 .. gamma^31
+  float pw[CHUNK];     // gamma^0 .. gamma^127; reverse: gamma^127 .. gamma^0
+  float pad[32];       // (read for columns that the mask leaves out)
+  // gamma^x in pw.
+  __device__ __forceinline__ int at(int x) const { return reverse ? CHUNK - 1 - x : x; }
 };
 constexpr uint32_t OFF_BAR = OFF_SEG + 2 * sizeof(Said);
 constexpr uint32_t OFF_TSLOT = OFF_BAR + 28 * 8;
@@ -198,19 +202,28 @@ __device__ __forceinline__ bool wait_handed(const int *flag, volatile int *abort
   }
 }
 
-// What the CTAs share evenly, where steps > 0: `steps` chunks of each of `units` units.  ticket[0] counts
-// the CTAs, ticket[1 + j] the state that CTA j hands on in slot j; all zero before the launch.
-struct Shared {
-  int units, steps;
+// The tiles' maps of a pass.
+struct Maps {
+  CUtensorMap x, y, w, out;
+};
+struct AllMaps {
+  Maps pass[lattn::MOST_PASSES];
+};
+// What a launch's CTAs take: `passes` passes over `units` units, the first one forward, the others in
+// reverse.  Where steps > 0 they share `steps` chunks of each unit of each pass evenly: ticket[0] counts the
+// CTAs, ticket[1 + j] the state that CTA j hands on in slot j; all zero before the launch.
+struct Work {
+  int passes, units, steps;
   int *ticket;
 };
 
-// STATE_ONLY: the segments' own states (y and w alone).
-template <bool REVERSE, bool STATE_ONLY>
+// STATE_ONLY: the segments' own states (y and w alone).  Only with BACKWARD are there passes in reverse (a
+// forward kernel that could go either way took 5 % longer).
+template <bool STATE_ONLY, bool BACKWARD>
 __global__ void __launch_bounds__(THREADS, 1)
-    attn_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY,
-                   const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmOut, const Params p,
-                   const Shared shared, const int inject_timeout) {
+    attn_tc_kernel(const __grid_constant__ AllMaps maps, const __grid_constant__ lattn::Passes ps,
+                   const __grid_constant__ Work work, const int inject_timeout) {
+  const Params &p = ps.p[0];  // but for tensors, states and factors the passes are alike
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(sm);
@@ -229,26 +242,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     *abort = 0;
     fence_mbarrier_init();
-    if (!STATE_ONLY) {
-      prefetch_tensormap(&tmX);
-      prefetch_tensormap(&tmOut);
+    for (int i = 0; i < work.passes; ++i) {
+      if (!STATE_ONLY) {
+        prefetch_tensormap(&maps.pass[i].x);
+        prefetch_tensormap(&maps.pass[i].out);
+      }
+      prefetch_tensormap(&maps.pass[i].y);
+      prefetch_tensormap(&maps.pass[i].w);
     }
-    prefetch_tensormap(&tmY);
-    prefetch_tensormap(&tmW);
   }
   if (warp == 2) {
     tmem_alloc(tslot, TMEM_COLS);
     tmem_relinquish();
   }
   int *number = reinterpret_cast<int *>(sm + OFF_NUMBER);
-  if (tid == 0) *number = shared.steps ? atomicAdd(shared.ticket, 1) : (int)blockIdx.x;
+  if (tid == 0) *number = work.steps ? atomicAdd(work.ticket, 1) : (int)blockIdx.x;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tb = *tslot;  // all columns are this CTA's: the base is 0, which the roles take as a constant
 
   const int cta = *number;
-  auto chunk_start = [](int nchunks, int c) { return (REVERSE ? nchunks - 1 - c : c) * CHUNK; };
+  auto chunk_start = [](const Said &g, int nchunks, int c) { return (BACKWARD && g.reverse ? nchunks - 1 - c : c) * CHUNK; };
   Said *segments = reinterpret_cast<Said *>(sm + OFF_SEG);
   // Segment k, as warp 3 says it; false: there is none, or a wait ran out.
   auto hear = [&](int k, bool &ok) {
@@ -269,9 +284,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int k = 0; hear(k, ok); ++k) {
       const Said &g = segments[k & 1];
       const int nchunks = g.nchunks;
+      const Maps &map = maps.pass[g.pass];
       if (lane == 0) {
         for (int c = 0; ok && c < nchunks; ++c, ++i) {
-          const int slot = i & 1, t0 = g.t_lo + chunk_start(nchunks, c);
+          const int slot = i & 1, t0 = g.t_lo + chunk_start(g, nchunks, c);
           const uint32_t par = (uint32_t)(i / 2 - 1) & 1u;
           auto load = [&](int full, int empty, uint32_t off, const CUtensorMap *map) {
             if (i > 1 && !wait(&bars[empty + slot], par, abort)) return false;
@@ -280,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             return true;
           };
           // (In the order in which a chunk's slots get free.)
-          ok = load(FY, EY, OFF_Y, &tmY) && (STATE_ONLY || load(FX, EX, OFF_X, &tmX)) && load(FW, EW, OFF_W, &tmW);
+          ok = load(FY, EY, OFF_Y, &map.y) && (STATE_ONLY || load(FX, EX, OFF_X, &map.x)) && load(FW, EW, OFF_W, &map.w);
         }
       }
       ok = __all_sync(0xffffffffu, ok);
@@ -301,24 +317,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---- segments -----------------------------------------------------------------------
     // One after the other, a segment ahead of the warps that take them: what leads from one segment to
     // the next is long, rarely run code, which would stand in the way of five roles.
+    // (A unit of pass i counts as unit i * units + unit here.)
     int unit_a = 0, step_a = 0, unit_b = 0, step_b = 0;  // the ends of a shared range
-    if (shared.steps) {
-      const long long all = (long long)shared.units * shared.steps;
+    if (work.steps) {
+      const long long all = (long long)work.passes * work.units * work.steps;
       const long long a = all * cta / gridDim.x, b = all * (cta + 1) / gridDim.x;
-      unit_a = (int)(a / shared.steps), step_a = (int)(a - (long long)unit_a * shared.steps);
-      unit_b = (int)(b / shared.steps), step_b = (int)(b - (long long)unit_b * shared.steps);
+      unit_a = (int)(a / work.steps), step_a = (int)(a - (long long)unit_a * work.steps);
+      unit_b = (int)(b / work.steps), step_b = (int)(b - (long long)unit_b * work.steps);
     }
     auto segment = [&](int idx, Said &g) {
       g.hand_to = -1;
-      if (!shared.steps) {
-        const int k = cta + idx * (int)gridDim.x;
-        if (k >= p.segments) return false;
-        const lattn::Segment o = lattn::segment_of<REVERSE>(p, p.first_segment + k);
+      if (!work.steps) {
+        int k = cta + idx * (int)gridDim.x;
+        if (k >= work.passes * p.segments) return false;
+        g.pass = k / p.segments;
+        g.reverse = BACKWARD && g.pass > 0;
+        k -= g.pass * p.segments;
+        const lattn::Segment o = lattn::segment_of<STATE_ONLY>(p, k, g.reverse);
         g.unit = o.unit, g.t_lo = o.t_lo, g.rows = o.rows, g.last = o.last, g.slot = o.slot;
       } else {
         const int whole0 = step_a ? unit_a + 1 : unit_a;
         const int k = idx - (step_b ? 1 : 0) + whole0;
-        int lo = 0, hi = shared.steps;
+        int lo = 0, hi = work.steps;
         if (step_b && idx == 0) {
           g.unit = unit_b;
           hi = step_b;
@@ -331,13 +351,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
           return false;
         }
-        g.t_lo = (REVERSE ? shared.steps - hi : lo) * CHUNK;
-        g.rows = min((REVERSE ? shared.steps - lo : hi) * CHUNK, p.T) - g.t_lo;
-        g.last = hi == shared.steps;
+        g.pass = g.unit / work.units;
+        g.reverse = BACKWARD && g.pass > 0;
+        g.unit -= g.pass * work.units;
+        g.t_lo = (g.reverse ? work.steps - hi : lo) * CHUNK;
+        g.rows = min((g.reverse ? work.steps - lo : hi) * CHUNK, p.T) - g.t_lo;
+        g.last = hi == work.steps;
         g.slot = lo ? cta - 1 : -1;
       }
       g.n = min(max(lattn::sequence_length(p.lengths, g.unit / p.H, p.T) - g.t_lo, 0), g.rows);
-      if (STATE_ONLY && g.last) g.n = 0;  // no segment follows it: its own state has no reader
       g.nchunks = (g.n + CHUNK - 1) / CHUNK;
       return true;
     };
@@ -353,15 +375,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       Said &to = segments[k & 1];
       const bool valid = segment(k, g);
       if (valid) {
-        g.log_decay = p.log_decay[g.unit % p.H];
-        for (int n = lane; n <= CHUNK; n += 32) to.pw[n] = decay_pow(g.log_decay, n);
-        to.ct[lane] = decay_pow(g.log_decay, REVERSE ? lane : 31 - lane);
+        const float ld = p.log_decay[g.unit % p.H];
+        g.full = decay_pow(ld, CHUNK);
+        for (int n = lane; n < CHUNK; n += 32) to.pw[g.at(n)] = decay_pow(ld, n);
+        to.ct[lane] = decay_pow(ld, g.reverse ? lane : 31 - lane);
       }
       if (lane == 0) {
         to.valid = valid;
         if (valid) {
-          to.unit = g.unit, to.t_lo = g.t_lo, to.rows = g.rows, to.n = g.n, to.nchunks = g.nchunks;
-          to.last = g.last, to.slot = g.slot, to.hand_to = g.hand_to, to.log_decay = g.log_decay;
+          to.pass = g.pass, to.reverse = g.reverse, to.unit = g.unit, to.t_lo = g.t_lo, to.rows = g.rows, to.n = g.n, to.nchunks = g.nchunks;
+          to.last = g.last, to.slot = g.slot, to.hand_to = g.hand_to, to.full = g.full;
         }
       }
       __syncwarp();
@@ -432,19 +455,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     // power of gamma is the product of one of the row's and one of the column's (ct), both at most 1.
     const int half = (warp - 4) >> 2;
     const uint32_t row = tmem_addr(0, 32 * w4, T_P), dst = tmem_addr(0, 32 * w4, T_PB);
-    const float2 a2 = make_float2(p.a, p.a);
     int i = 0;
     for (int k = 0; hear(k, ok); ++k) {
       const Said &g = segments[k & 1];
       const int nchunks = g.nchunks, ntok = g.n;
+      auto reverse = [&]() { return BACKWARD && g.reverse; };  // (not kept: a register is worth more than a read)
+      const float a = ps.p[BACKWARD ? g.pass : 0].a;
       const float *pw = g.pw, *ct = g.ct;
       for (int c = 0; c < nchunks; ++c, ++i) {
-        const int n = min(CHUNK, ntok - chunk_start(nchunks, c));
+        const int n = min(CHUNK, ntok - chunk_start(g, nchunks, c));
         if (!(ok = wait_warp(&bars[PFULL], (uint32_t)i & 1u, abort))) break;
         tc_fence_after_sync();
 #pragma unroll 1
         for (int j = 2 * half; j < 2 * half + 2; ++j) {
-          const int d = REVERSE ? j - w4 : w4 - j;
+          const int d = reverse() ? j - w4 : w4 - j;
           uint32_t pk[16];
           if (d < 0) {
 #pragma unroll
@@ -452,10 +476,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           } else {
             uint32_t r[32];
             tmem_ld_32x32b_x32(row + 32 * j, r);
-            const int end = REVERSE ? n - 32 * j : 32;  // columns that hold tokens (forward: s <= t decides)
-            if (d == 0 || end < 32) {
-              const float *f = pw + (REVERSE ? 32 * d - lane : 32 * d + lane);
-              const int most = REVERSE ? end : 32 * d + lane + 1, least = REVERSE ? lane - 32 * d : 0;
+            // The columns that count: s <= t, or, in reverse, s >= t and of a token.
+            const int least = reverse() ? lane - 32 * d : 0, most = reverse() ? n - 32 * j : 32 * d + lane + 1;
+            if (d == 0 || (reverse() && most < 32)) {
+              // gamma^(t - s), or gamma^(s - t): in pw, backwards from here.
+              const float *f = pw + (reverse() ? CHUNK - 1 - 32 * d : 32 * d) + lane;
+              const float2 a2 = make_float2(a, a);
               tmem_wait_ld();
               loaded(r);
 #pragma unroll
@@ -464,14 +490,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const int s = 2 * e + h;
-                  const bool in = s < most && s >= least;
-                  v[h] = in ? __uint_as_float(r[s]) * f[REVERSE ? s : -s] : 0.f;
+                  v[h] = s < most && s >= least ? __uint_as_float(r[s]) * f[-s] : 0.f;
                 }
                 const float2 u = __fmul2_rn(a2, make_float2(v[0], v[1]));
                 pk[e] = pack_bf16x2(u.x, u.y);
               }
             } else {
-              const float b = p.a * pw[REVERSE ? 32 * d - lane : lane + 32 * d - 31];
+              const float b = a * pw[reverse() ? CHUNK - 1 - 32 * d + lane : lane + 32 * d - 31];
               const float2 b2 = make_float2(b, b);
               tmem_wait_ld();
               loaded(r);
@@ -508,9 +533,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int k = 0; hear(k, ok); ++k) {
       const Said &g = segments[k & 1];
       const int nchunks = g.nchunks, ntok = g.n;
-      const float h_full = p.e * g.pw[REVERSE ? s + 1 : CHUNK - 1 - s];
+      auto reverse = [&]() { return BACKWARD && g.reverse; };  // (not kept: a register is worth more than a read)
+      const float e = ps.p[BACKWARD ? g.pass : 0].e;
+      // (gamma^(s + 1) of the last row in reverse is gamma^128, which has a place of its own.)
+      const float h_full = e * (!reverse() ? g.pw[CHUNK - 1 - s] : s == CHUNK - 1 ? g.full : g.pw[g.at(s + 1)]);
       for (int c = 0; ok && c < nchunks; ++c, ++i) {
-        const int n = min(CHUNK, ntok - chunk_start(nchunks, c));
+        const int n = min(CHUNK, ntok - chunk_start(g, nchunks, c));
         const uint32_t slot = i & 1, par2 = (uint32_t)(i >> 1) & 1u;
         uint8_t *ty = sm + OFF_Y + slot * TILE;
         uint8_t *ys = sm + OFF_YS + slot * (3 * TILE);
@@ -519,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (i > 1 && !(ok = wait_warp(&bars[MFULL + slot], par2 ^ 1u, abort))) break;
         float h1 = h_full;
         if (n < CHUNK) {
-          if (!REVERSE) h1 = p.e * g.pw[max(n - 1 - s, 0)];
+          if (!reverse()) h1 = e * g.pw[max(n - 1 - s, 0)];
           if (!(ok = wait_warp(&bars[FW + slot], par2, abort))) break;
           if (s >= n) {
 #pragma unroll 1
@@ -571,9 +599,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int nchunks = g.nchunks, ntok = g.n;
       float C[32];
       {
-        if (shared.steps && g.slot >= 0 && !(ok = wait_handed(shared.ticket + 1 + g.slot, abort))) break;
-        const float *C0 = lattn::start_state(p, g.unit, g.slot);
-        const bool as_is = p.transposed || (shared.steps && g.slot >= 0);
+        // (A state handed on lies as this kernel carries it, C^T.)
+        const bool handed = work.steps && g.slot >= 0;
+        if (handed && !(ok = wait_handed(work.ticket + 1 + g.slot, abort))) break;
+        const float *C0 = lattn::start_state(ps.p[g.pass], g.unit, handed ? g.slot : g.slot);
+        const bool as_is = ps.p[g.pass].transposed || handed;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int r = row + 8 * ((e >> 1) & 1), cc = 8 * (e >> 2) + col + (e & 1);
@@ -594,8 +624,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[CREADY]);
-        const int n = min(CHUNK, ntok - chunk_start(nchunks, c));
-        const float dn = g.pw[n];
+        const int n = min(CHUNK, ntok - chunk_start(g, nchunks, c));
+        const float dn = n == CHUNK ? g.full : g.pw[BACKWARD ? g.at(n) : n];
         if (!(ok = wait_warp(&bars[MFULL + (i & 1)], (uint32_t)(i >> 1) & 1u, abort))) break;
         tc_fence_after_sync();
 #pragma unroll
@@ -616,13 +646,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      // (A state handed on lies as this kernel carries it, C^T.)
       if (g.hand_to >= 0) {
-        float *Co = p.slots + (long long)g.hand_to * (D * D);
+        float *Co = p.slots + (long long)(g.hand_to) * (D * D);
 #pragma unroll
         for (int e = 0; e < 32; ++e) Co[(row + 8 * ((e >> 1) & 1)) * D + 8 * (e >> 2) + col + (e & 1)] = C[e];
-        hand_on(shared.ticket + 1 + g.hand_to);
-      } else if (float *Co = lattn::end_state(p, g.unit, g.slot, g.last)) {
+        hand_on(work.ticket + 1 + g.hand_to);
+      } else if (float *Co = lattn::end_state(ps.p[g.pass], g.unit, g.slot, g.last)) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) Co[(8 * (e >> 2) + col + (e & 1)) * D + row + 8 * ((e >> 1) & 1)] = C[e];
       }
@@ -636,8 +665,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Said &g = segments[k & 1];
       const int nchunks = g.nchunks, ntok = g.n;
       for (int c = 0; c < nchunks; ++c, ++i) {
-        const int c0 = chunk_start(nchunks, c), n = min(CHUNK, ntok - c0);
-        const float f1 = p.c * g.pw[REVERSE ? max(n - 1 - t, 0) : t + 1];
+        const int c0 = chunk_start(g, nchunks, c), n = min(CHUNK, ntok - c0);
+        const int x = BACKWARD && g.reverse ? max(n - 1 - t, 0) : t + 1;
+        const float f1 = ps.p[BACKWARD ? g.pass : 0].c * (x == CHUNK ? g.full : g.pw[BACKWARD ? g.at(x) : x]);
         const float2 f = make_float2(f1, f1);
         if (!(ok = wait_warp(&bars[OFULL], (uint32_t)i & 1u, abort))) break;
         tc_fence_after_sync();
@@ -671,11 +701,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
           mbar_arrive(&bars[OFREE]);
           const int t0 = g.t_lo + c0 + 32 * w4;
-          if (t0 < p.T) tma_store_3d(&tmOut, sm + OFF_OUT + 32 * w4 * 128, 0, t0, g.unit);
+          if (t0 < p.T) tma_store_3d(&maps.pass[g.pass].out, sm + OFF_OUT + 32 * w4 * 128, 0, t0, g.unit);
         }
       }
       // Rows of chunks wholly behind the end (those of the last chunk are in its tile).
-      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + ((long long)g.unit * p.T + g.t_lo) * D;
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(ps.p[g.pass].out) + ((long long)g.unit * p.T + g.t_lo) * D;
       const int x0 = min(nchunks * CHUNK, g.rows) * (D / 8), x1 = g.rows * (D / 8);
       for (int x = x0 + (tid & 127); x < x1; x += 128)
         reinterpret_cast<uint4 *>(out)[x] = make_uint4(0u, 0u, 0u, 0u);

@@ -740,65 +740,75 @@ int check_buffers(std::initializer_list<Buffer> ins, std::initializer_list<Buffe
   return TTT_OK;
 }
 
-// How the units (batch x heads) are dealt out to the SMs.
+// How the units (batch x heads) are dealt out to the SMs.  A call has one pass over them (forward) or three
+// (backward, in one launch, since they have no part in one another).
 //
-// (Segments at a time: one an SM of the tensor-core kernel, two of the CUDA-core kernel; "SMs" below.)
+// Tensor-core kernel, more units (of all passes) than SMs: the CTAs share all chunks evenly (`steps` chunks a
+// unit, see tc_linear_attn.cuh), unless whole units come out even.
 //
-// More units than SMs, tensor-core kernel: the CTAs share all chunks evenly (`steps` chunks a unit, see
-// tc_linear_attn.cuh), unless whole units come out even.  Measured on one B200 against whole units
-// alone: see there.
-//
-// Fewer units than SMs (and what would be left for the last, unfilled round of the CUDA-core kernel): they
-// may be cut into segments that fill the SMs, which costs a pass over half of their inputs for the
-// segments' own states.  The cut with the least time is taken, in steps of one chunk on one SM: each of
-// the call's passes takes ceil(segments / SMs) rounds, as does each of its state passes, a step of which
-// takes ATTN_STATE_STEP of a full one; ATTN_SEGMENT_STEPS go to each segment's start and end and
-// ATTN_CUT_STEPS to the two more launches of a state pass.
+// Fewer units (CUDA-core kernel: what is left for its last, unfilled round): they may be cut into
+// segments that fill the SMs, which costs a pass over half of their inputs for the segments' own
+// states.  The cut with the least time is taken, counted in steps (a chunk of one segment) as measured on
+// one B200: a state pass's step takes 0.65 of a full one (CUDA cores 0.5), a segment's start and end 0.7,
+// the two more launches 4 (0.4, of a step that is ten times as long); two segments an SM at a time, which
+// only the CUDA-core kernel takes, 1.6 times as long as one, more of them 0.8 of their number and a bit.
+// Forward and backward, us, for 1 to 32 segments a unit:
+//   bf16 B1 H32 T32768  1: 421, 4: 189, 9: 181 (taken), 18: 196      1: 445, 4: 488, 9: 469
+//   bf16 B1 H12 T4096   1: 59, 4: 37, 8: 27, 12: 27, 24: 32          1: 63, 4: 40 (taken), 8: 45, 16: 52
+//   fp32 B6 H8 T1999    1: 266, 4: 158, 6: 124 (taken), 8: 161       1: 265 (taken), 2: 302, 6: 322
+//   fp32 B3 H5 T777     1: 105, 2: 97, 4: 53, 7: 32 (taken)          1: 109, 4: 76, 7: 56 (taken)
 struct AttnPlan {
   lattn::Cut cut;
-  int steps;           // > 0: the CTAs share the chunks
-  size_t slots_bytes;  // one set of segment states, or the states that CTAs hand on
-  size_t ticket_bytes; // one pass's counters, after the slots
+  int steps;            // > 0: the CTAs share the chunks
+  size_t slots_bytes;   // one set of segment states (a backward has two), or all states that CTAs hand on
+  size_t ticket_bytes;  // the CTAs' counters, after the slots
+  size_t bytes;         // of workspace
 };
 constexpr int ATTN_SMS = 148;          // SMs of a B200: the workspace size does not ask a device
 constexpr int ATTN_CUDA_CORE_CTAS = 2;  // CTAs of the CUDA-core kernel an SM
 constexpr int ATTN_CHUNK = 128;        // tokens of a step
 constexpr int ATTN_MOST_SEGMENTS = 64;
-constexpr double ATTN_STATE_STEP = 0.55;
-constexpr double ATTN_SEGMENT_STEPS = 0.7;
-constexpr double ATTN_CUT_STEPS = 4;
 static_assert(ATTN_CHUNK == tclattn::CHUNK && ATTN_CHUNK % lattn::CHUNK == 0, "segments are whole chunks");
 AttnPlan attn_plan(long long units, int T, bool backward, bool tensor_cores) {
-  AttnPlan best{{(int)units, 1, T > 0 ? T : 1}, 0, 0, 0};
-  const long long slots = ATTN_SMS * (tensor_cores ? 1 : ATTN_CUDA_CORE_CTAS);  // segments at a time
-  const long long left = units % slots, chunks = ((long long)T + ATTN_CHUNK - 1) / ATTN_CHUNK;
-  if (left == 0 || chunks < 2) return best;
-  if (tensor_cores && units > ATTN_SMS) {
+  AttnPlan best{{(int)units, 1, T > 0 ? T : 1}, 0, 0, 0, 0};
+  const int passes = backward ? 3 : 1;
+  const long long chunks = ((long long)T + ATTN_CHUNK - 1) / ATTN_CHUNK;
+  const long long most = tensor_cores ? ATTN_SMS : ATTN_SMS * ATTN_CUDA_CORE_CTAS;  // segments at a time
+  if (chunks < 2 || passes * units % most == 0) return best;
+  if (tensor_cores && passes * units > ATTN_SMS) {
     best.steps = (int)chunks;
     best.slots_bytes = (size_t)ATTN_SMS * lattn::D * lattn::D * 4;
-    best.ticket_bytes = (size_t)align16(4 * (1 + ATTN_SMS));
+    best.ticket_bytes = align16(4 * (1 + ATTN_SMS));
+    best.bytes = best.slots_bytes + best.ticket_bytes;
     return best;
   }
-  const int passes = backward ? 3 : 1, states = backward ? 2 : 1;
-  auto rounds = [&](long long n) { return (double)((n + slots - 1) / slots); };
-  double least = passes * (chunks + ATTN_SEGMENT_STEPS);
+  const long long left = tensor_cores ? units : units % most;
+  if (left == 0) return best;
+  const double state_step = tensor_cores ? 0.65 : 0.5, ends = 0.7, cut_steps = tensor_cores ? 4 : 0.4;
+  auto rounds = [&](long long n) {
+    const long long r = (n + ATTN_SMS - 1) / ATTN_SMS;
+    return tensor_cores || r < 2 ? (double)r : r == 2 ? 1.6 : 0.8 * ((double)n / ATTN_SMS + 0.35);
+  };
+  double least = rounds(passes * left) * (chunks + ends);
   for (int n = 2; n <= ATTN_MOST_SEGMENTS && n <= chunks; ++n) {
     const long long len = (chunks + n - 1) / n, nseg = (chunks + len - 1) / len;
     if (nseg != n) continue;
-    const double cost =
-        passes * rounds(left * n) * (len + ATTN_SEGMENT_STEPS) +
-        states * (rounds(left * (n - 1)) * (len * ATTN_STATE_STEP + ATTN_SEGMENT_STEPS) + ATTN_CUT_STEPS);
+    const double cost = rounds(passes * left * n) * (len + ends) +
+                        rounds((backward ? 2 : 1) * left * (n - 1)) * (len * state_step + ends) + cut_steps;
     if (cost < least) {
       least = cost;
       best.cut = {(int)(units - left), n, (int)(len * ATTN_CHUNK)};
       best.slots_bytes = (size_t)left * n * lattn::D * lattn::D * 4;
+      best.bytes = best.slots_bytes * (backward ? 2 : 1);
     }
   }
   return best;
 }
-// Forward: slots, counters.  Backward: two sets of slots, three passes' counters.
-size_t attn_workspace(const AttnPlan &plan, bool backward) {
-  return plan.slots_bytes * (backward ? 2 : 1) + plan.ticket_bytes * (backward ? 3 : 1);
+
+// What callers are told and held to: enough for either kernel, since which one runs depends on the inputs'
+// type and the path setting too.
+size_t attn_workspace_bytes(long long units, int T, bool backward) {
+  return std::max(attn_plan(units, T, backward, true).bytes, attn_plan(units, T, backward, false).bytes);
 }
 
 template <typename KernelT, typename ParamsT>
@@ -812,57 +822,77 @@ int launch_attn(KernelT kernel, long long grid, int threads, size_t smem, cudaSt
   return TTT_OK;
 }
 
-template <bool REVERSE, bool STATE_ONLY>
-int launch_attn_tc(long long units, const lattn::Params &p, int steps, int *ticket, cudaStream_t s) {
-  CUtensorMap mx, my, mw, mo;
-  if (!make_qkv_map(&my, p.Y, p.T, units, tclattn::CHUNK) || !make_qkv_map(&mw, p.W, p.T, units, tclattn::CHUNK) ||
-      !make_qkv_map(&mx, STATE_ONLY ? p.Y : p.X, p.T, units, tclattn::CHUNK) ||
-      !make_qkv_map(&mo, STATE_ONLY ? p.Y : p.out, p.T, units, tclattn::OUT_ROWS))
-    return TTT_ERR_CUDA;
-  auto kernel = tclattn::attn_tc_kernel<REVERSE, STATE_ONLY>;
+bool attn_on_tensor_cores(bool bf16, int T) { return bf16 && T > 0 && g_path.load() != TTT_PATH_SIMT; }
+
+bool make_attn_maps(tclattn::Maps *m, const lattn::Params &p, long long units) {
+  const bool state_only = p.slots_out != nullptr;
+  return make_qkv_map(&m->y, p.Y, p.T, units, tclattn::CHUNK) && make_qkv_map(&m->w, p.W, p.T, units, tclattn::CHUNK) &&
+         make_qkv_map(&m->x, state_only ? p.Y : p.X, p.T, units, tclattn::CHUNK) &&
+         make_qkv_map(&m->out, state_only ? p.Y : p.out, p.T, units, tclattn::OUT_ROWS);
+}
+
+// One launch: n = 1 pass (forward), 2 (states for a backward: one forward, one reverse) or 3 (a
+// backward's: one forward, two reverse).  `ticket`: a shared launch's zeroed counters.
+int attn_passes(bool bf16, bool tc, int n, long long units, const AttnPlan &plan, lattn::Passes ps, int *ticket,
+                cudaStream_t s) {
+  const bool state_only = ps.p[0].slots_out != nullptr;
+  for (int i = 0; i < lattn::MOST_PASSES; ++i) {
+    ps.p[i].segments = i < n ? ps.p[i].cut.segments((int)units, state_only) : 0;
+  }
+  const int segments = ps.p[0].segments;
+  if (!tc) {
+    auto kernel = bf16 ? (state_only ? lattn::attn_kernel<__nv_bfloat16, true> : lattn::attn_kernel<__nv_bfloat16, false>)
+                       : (state_only ? lattn::attn_kernel<float, true> : lattn::attn_kernel<float, false>);
+    return launch_attn(kernel, (long long)n * segments, lattn::THREADS, lattn::SMEM_BYTES, s, ps);
+  }
+  tclattn::AllMaps maps;
+  for (int i = 0; i < n; ++i)
+    if (!make_attn_maps(&maps.pass[i], ps.p[i], units)) return TTT_ERR_CUDA;
+  auto kernel = n == 1 ? (state_only ? tclattn::attn_tc_kernel<true, false> : tclattn::attn_tc_kernel<false, false>)
+                       : (state_only ? tclattn::attn_tc_kernel<true, true> : tclattn::attn_tc_kernel<false, true>);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tclattn::SMEM_BYTES) != cudaSuccess)
     return TTT_ERR_CUDA;
-  kernel<<<(unsigned)std::min(p.segments, ATTN_SMS), tclattn::THREADS, tclattn::SMEM_BYTES, s>>>(
-      mx, my, mw, mo, p, tclattn::Shared{(int)units, steps, ticket}, g_inject_timeout.load());
+  const long long ctas = std::min<long long>((long long)n * segments, ATTN_SMS);
+  kernel<<<(unsigned)ctas, tclattn::THREADS, tclattn::SMEM_BYTES, s>>>(
+      maps, ps, tclattn::Work{n, (int)units, plan.steps, ticket}, g_inject_timeout.load());
   if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return TTT_OK;
 }
 
-bool attn_on_tensor_cores(bool bf16, int T) { return bf16 && T > 0 && g_path.load() != TTT_PATH_SIMT; }
-
-// One pass over all units (or, for states alone, over the cut ones).  A shared pass takes zeroed counters.
-int attn_pass(bool bf16, bool tc, bool reverse, long long units, lattn::Params p, int steps, int *ticket,
-              cudaStream_t s) {
-  const bool state_only = p.slots_out != nullptr;
-  p.first_segment = state_only ? p.cut.whole : 0;
-  p.segments = p.cut.segments((int)units) - p.first_segment;
-  if (tc) {
-    auto run = state_only ? (reverse ? launch_attn_tc<true, true> : launch_attn_tc<false, true>)
-                          : (reverse ? launch_attn_tc<true, false> : launch_attn_tc<false, false>);
-    return run(units, p, steps, ticket, s);
+// A call's launches: for cut units the segments' own states and the scan that turns them into the states
+// that the segments start from; for shared chunks the counters; then the passes.
+int attn_run(bool bf16, bool tc, int n, long long units, const AttnPlan &plan, lattn::Passes ps, void *workspace,
+             cudaStream_t s) {
+  float *slots = static_cast<float *>(workspace);
+  int *ticket = nullptr;
+  for (int i = 0; i < n; ++i)
+    ps.p[i].slots = slots && !plan.steps && i > 0 ? slots + plan.slots_bytes / 4 : slots;
+  if (plan.steps) {
+    ticket = reinterpret_cast<int *>(slots + plan.slots_bytes / 4);
+    if (cudaMemsetAsync(ticket, 0, plan.ticket_bytes, s) != cudaSuccess) return TTT_ERR_CUDA;
+  } else if (plan.slots_bytes) {
+    // The forward pass's states come from its y, w (dQ: of V, K taken as K, V: its carried state is the
+    // transpose of theirs), the reverse passes' from the last one's.
+    const int states = n == 1 ? 1 : 2;
+    lattn::Passes own = ps;
+    if (n == 3) {
+      std::swap(own.p[0].Y, own.p[0].W);
+      own.p[1] = ps.p[2];
+    }
+    for (int i = 0; i < states; ++i) {
+      own.p[i].slots_out = ps.p[i].slots;
+      own.p[i].transposed = false;
+    }
+    int st = attn_passes(bf16, tc, states, units, plan, own, nullptr, s);
+    if (st != TTT_OK) return st;
+    const lattn::Params &f = ps.p[0], &r = ps.p[n - 1];
+    const int blocks = (int)(units - plan.cut.whole) * 4;
+    lattn::ScanParams sp{{f.slots, r.slots}, {f.C0, r.C0}, f.log_decay, f.lengths, f.H, f.T, plan.cut, blocks};
+    st = launch_attn(lattn::scan_kernel, states * blocks, lattn::SCAN_THREADS, 0, s, sp);
+    if (st != TTT_OK) return st;
   }
-  auto kernel = [&] {
-    if (state_only)
-      return bf16 ? (reverse ? lattn::attn_kernel<__nv_bfloat16, true, true> : lattn::attn_kernel<__nv_bfloat16, false, true>)
-                  : (reverse ? lattn::attn_kernel<float, true, true> : lattn::attn_kernel<float, false, true>);
-    return bf16 ? (reverse ? lattn::attn_kernel<__nv_bfloat16, true, false> : lattn::attn_kernel<__nv_bfloat16, false, false>)
-                : (reverse ? lattn::attn_kernel<float, true, false> : lattn::attn_kernel<float, false, false>);
-  }();
-  return launch_attn(kernel, p.segments, lattn::THREADS, lattn::SMEM_BYTES, s, p);
-}
-
-// The states that the cut units' segments start from, into `slots`: the segments' own states, then the scan.
-int attn_segment_states(bool bf16, bool tc, bool reverse, long long units, const AttnPlan &plan, const void *Y, const void *W,
-                        float e, const float *log_decay, const int *lengths, const float *C0, int H, int T,
-                        float *slots, cudaStream_t s) {
-  lattn::Params p{Y, Y, W, log_decay, lengths, nullptr, nullptr, false, 0.f, 0.f, e, nullptr, nullptr, slots, H, T,
-                  plan.cut, 0, 0};
-  int st = attn_pass(bf16, tc, reverse, units, p, 0, nullptr, s);
-  if (st != TTT_OK) return st;
-  lattn::ScanParams sp{slots, C0, log_decay, lengths, H, T, plan.cut};
-  return launch_attn(reverse ? lattn::scan_kernel<true> : lattn::scan_kernel<false>, (units - plan.cut.whole) * 4,
-                     lattn::SCAN_THREADS, 0, s, sp);
+  return attn_passes(bf16, tc, n, units, plan, ps, ticket, s);
 }
 
 // Sizes shared by the linear attention entry points over sequences.
@@ -888,25 +918,15 @@ int run_attn_fwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
   const size_t xb = (size_t)units * T * d * (bf16 ? 2 : 4), sb = (size_t)units * d * d * 4;
   const bool tc = attn_on_tensor_cores(bf16, T);
   const AttnPlan plan = attn_plan(units, T, false, tc);
-  const size_t wb = attn_workspace(plan, false);
+  const size_t wb = attn_workspace_bytes(units, T, false);
   if (wb && (!workspace || workspace_bytes < wb)) return TTT_ERR_ARG;
   st = check_buffers({{Q, xb, tok}, {K, xb, tok}, {V, xb, tok}, {log_decay, (size_t)H * 4, true}, {S0, sb, false},
                       {lengths, (size_t)B * 4, false}},
                      {{Z, xb, tok}, {S_out, sb, false}, {wb ? workspace : nullptr, wb, false}});
   if (st != TTT_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  float *slots = static_cast<float *>(workspace);
-  int *ticket = nullptr;
-  if (plan.steps) {
-    ticket = reinterpret_cast<int *>(slots + plan.slots_bytes / 4);
-    if (cudaMemsetAsync(ticket, 0, plan.ticket_bytes, s) != cudaSuccess) return TTT_ERR_CUDA;
-  } else if (plan.slots_bytes) {
-    st = attn_segment_states(bf16, tc, false, units, plan, K, V, 1.f, log_decay, lengths, S0, H, T, slots, s);
-    if (st != TTT_OK) return st;
-  }
-  lattn::Params p{Q, K, V, log_decay, lengths, S0, slots, false, scale, scale, 1.f, Z, S_out, nullptr, H, T,
-                  plan.cut, 0, 0};
-  return attn_pass(bf16, tc, false, units, p, plan.steps, ticket, s);
+  lattn::Passes ps{{{Q, K, V, log_decay, lengths, S0, nullptr, false, scale, scale, 1.f, Z, S_out, nullptr, H, T, plan.cut,
+                     0}}};
+  return attn_run(bf16, tc, 1, units, plan, ps, wb ? workspace : nullptr, static_cast<cudaStream_t>(stream));
 }
 
 int run_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype, const float *log_decay, const float *S0,
@@ -921,37 +941,20 @@ int run_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype, con
   const size_t xb = (size_t)units * T * d * (bf16 ? 2 : 4), sb = (size_t)units * d * d * 4;
   const bool tc = attn_on_tensor_cores(bf16, T);
   const AttnPlan plan = attn_plan(units, T, true, tc);
-  const size_t wb = attn_workspace(plan, true);
+  const size_t wb = attn_workspace_bytes(units, T, true);
   if (wb && (!workspace || workspace_bytes < wb)) return TTT_ERR_ARG;
   st = check_buffers({{Q, xb, tok}, {K, xb, tok}, {V, xb, tok}, {dZ, xb, tok}, {log_decay, (size_t)H * 4, true},
                       {S0, sb, false}, {dS_T, sb, false}, {lengths, (size_t)B * 4, false}},
                      {{dQ, xb, tok}, {dK, xb, tok}, {dV, xb, tok}, {dS0, sb, false}, {wb ? workspace : nullptr, wb, false}});
   if (st != TTT_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  float *slots_s = static_cast<float *>(workspace), *slots_g = nullptr;
-  int *ticket[3] = {};
-  if (plan.slots_bytes) slots_g = slots_s + plan.slots_bytes / 4;
-  if (plan.steps) {
-    char *at = reinterpret_cast<char *>(slots_g) + plan.slots_bytes;
-    for (int i = 0; i < 3; ++i) ticket[i] = reinterpret_cast<int *>(at + i * plan.ticket_bytes);
-    if (cudaMemsetAsync(at, 0, 3 * plan.ticket_bytes, s) != cudaSuccess) return TTT_ERR_CUDA;
-  } else if (plan.slots_bytes) {
-    st = attn_segment_states(bf16, tc, false, units, plan, K, V, 1.f, log_decay, lengths, S0, H, T, slots_s, s);
-    if (st != TTT_OK) return st;
-    st = attn_segment_states(bf16, tc, true, units, plan, Q, dZ, scale, log_decay, lengths, dS_T, H, T, slots_g, s);
-    if (st != TTT_OK) return st;
-  }
-  lattn::Params pq{dZ, V, K, log_decay, lengths, S0, slots_s, true, scale, scale, 1.f, dQ, nullptr, nullptr, H, T,
-                   plan.cut, 0, 0};
-  lattn::Params pk{V, dZ, Q, log_decay, lengths, dS_T, slots_g, true, scale, 1.f, scale, dK, nullptr, nullptr, H, T,
-                   plan.cut, 0, 0};
-  lattn::Params pv{K, Q, dZ, log_decay, lengths, dS_T, slots_g, false, scale, 1.f, scale, dV, dS0, nullptr, H, T,
-                   plan.cut, 0, 0};
-  if (tok) {
-    if ((st = attn_pass(bf16, tc, false, units, pq, plan.steps, ticket[0], s)) != TTT_OK) return st;
-    if ((st = attn_pass(bf16, tc, true, units, pk, plan.steps, ticket[1], s)) != TTT_OK) return st;
-  }
-  return attn_pass(bf16, tc, true, units, pv, plan.steps, ticket[2], s);
+  // dQ forward, dK and dV in reverse (see linear_attn.cuh).
+  lattn::Passes ps{{{dZ, V, K, log_decay, lengths, S0, nullptr, true, scale, scale, 1.f, dQ, nullptr, nullptr, H, T,
+                     plan.cut, 0},
+                    {V, dZ, Q, log_decay, lengths, dS_T, nullptr, true, scale, 1.f, scale, dK, nullptr, nullptr, H, T,
+                     plan.cut, 0},
+                    {K, Q, dZ, log_decay, lengths, dS_T, nullptr, false, scale, 1.f, scale, dV, dS0, nullptr, H, T,
+                     plan.cut, 0}}};
+  return attn_run(bf16, tc, 3, units, plan, ps, wb ? workspace : nullptr, static_cast<cudaStream_t>(stream));
 }
 
 // The rotary arguments of a call.  TTT_OK and rotary_dim == 0: no rotation.
@@ -1439,10 +1442,7 @@ int ttt_linear_ln_decode(const void *q, const void *k, const void *v, int qkv_dt
 
 size_t ttt_linear_attn_workspace_bytes(int B, int H, int T, int d, int backward) {
   if (B < 0 || H < 0 || T < 0 || check_attn_sizes(TTT_F32, 1.f, B, H, T, d) != TTT_OK) return 0;
-  const long long units = (long long)B * H;
-  // Enough for either kernel: which one runs depends on the inputs' type and the path setting too.
-  return std::max(attn_workspace(attn_plan(units, T, backward != 0, true), backward != 0),
-                  attn_workspace(attn_plan(units, T, backward != 0, false), backward != 0));
+  return attn_workspace_bytes((long long)B * H, T, backward != 0);
 }
 
 int ttt_linear_attn_fwd(const void *Q, const void *K, const void *V, int qkv_dtype, const float *log_decay,
