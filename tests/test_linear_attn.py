@@ -268,6 +268,41 @@ def test_many_chunks_and_segments_on_both_paths(size, decay):
                 assert bool((over <= 1e-30).all()), (n, float(over.max()))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,T", [(64, 7, 70), (64, 7, 300), (9, 40, 513)])
+def test_padded_batches_of_many_sequences(dtype, B, H, T):
+    """Many units an SM, among them empty ones, one after another: the pipelines run on over them."""
+    rng = np.random.default_rng(8)
+    lengths = rng.integers(0, T + 1, B)
+    lengths[rng.permutation(B)[: B // 2]] = 0
+    lengths[:4] = (T, 0, 0, 0)
+    c = make(B, H, T, dtype, "slow", True, lengths=lengths, back=True)
+    x = device(c, dtype)
+    for fn, run in (("fwd", run_fwd), ("bwd", run_bwd)):
+        ref = reference(c, fn)
+        check(run(x), ref, bounds(c, fn, dtype, ref))
+    assert ttt.last_device_status() == 0
+
+
+def test_an_expired_wait_is_reported():
+    """Every CTA's first wait runs out (nothing arrives there): the calls come back, the status says so once,
+    and the next calls are right."""
+    c = make(6, 30, 300, "bf16", "slow", True, back=True, lengths=[300, 0, 7, 128, 299, 1])
+    x = device(c, "bf16")
+    want = {**run_fwd(x), **run_bwd(x)}
+    ttt.debug_inject_timeout(True)
+    try:
+        run_fwd(x), run_bwd(x)
+        assert ttt.last_device_status() == ttt.TTT_ERR_TIMEOUT
+    finally:
+        ttt.debug_inject_timeout(False)
+    assert ttt.last_device_status() == 0
+    got = {**run_fwd(x), **run_bwd(x)}
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    assert ttt.last_device_status() == 0
+
+
 # ---- calls a user makes that the sizes do not show ------------------------------------------
 
 def test_results_do_not_change_between_calls():
