@@ -151,19 +151,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, wait(bar, parity, abort));
 }
 
-// Whether the phase is complete, without waiting.
-__device__ __forceinline__ bool is_complete(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // x less a pair of bf16 numbers, exact for the numbers nearest to x.
 __device__ __forceinline__ float2 minus_bf16x2(float2 x, uint32_t b) {
   float2 d;
@@ -445,27 +432,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       issue<4>(T_XC, smem_desc_sw128(sbase + OFF_X + slot * TILE, 16, 1024), 32,
                smem_desc_sw128(sbase + OFF_C + slot * C_BYTES, 16, 1024), 32, ID_XC);
       if (i + 2 < total) umma_commit_w(&bars[EX + slot]);
-      // P is read and its bf16 form written: the next chunk's P, if its tiles are in (its warps have the
-      // longest work before them), and P w.  P w must not wait for them: where the next chunk lies behind
-      // empty segments, they come only when every warp is done with this one's segment.
+      // P is read and its bf16 form written: P w, then the next chunk's P.  (In this order: where the next
+      // chunk lies behind empty segments, its tiles come only when every warp is done with this one's
+      // segment, the output warps among them.)
       if (!(ok = wait_warp(&bars[PREADY], par, abort))) break;
-      const uint32_t next = slot ^ 1u, par2_next = (uint32_t)((i + 1) >> 1) & 1u;
-      const bool more = i + 1 < total;
-      const bool early = __all_sync(0xffffffffu, more && is_complete(&bars[FX + next], par2_next) &&
-                                                     is_complete(&bars[FY + next], par2_next));
-#pragma unroll 1
-      for (int turn = 0; turn < 2; ++turn) {
-        if ((turn == 0) == early) {
-          if (more && !(ok = scores(i + 1))) break;
-        } else {
-          tc_fence_after_sync();
-          const uint64_t b = smem_desc_sw128(w, 8192, 1024);
+      tc_fence_after_sync();
+      {
+        const uint64_t b = smem_desc_sw128(w, 8192, 1024);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) umma_ts_w(T_PW, T_PB + 8 * k, b + k * (2048 >> 4), ID_PW, k > 0);
-          umma_commit_w(&bars[OFULL]);
-          if (i + 2 < total) umma_commit_w(&bars[EW + slot]);
-        }
+        for (int k = 0; k < 8; ++k) umma_ts_w(T_PW, T_PB + 8 * k, b + k * (2048 >> 4), ID_PW, k > 0);
       }
+      umma_commit_w(&bars[OFULL]);
+      if (i + 2 < total) umma_commit_w(&bars[EW + slot]);
+      if (i + 1 < total && !(ok = scores(i + 1))) break;
     }
     __syncwarp();
     if (*abort) {  // products in flight end before the tensor memory is freed
