@@ -8,6 +8,7 @@ is no CPU path: tensors that are not on a CUDA device are rejected.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -76,6 +77,19 @@ def _call(name, device, *args):
         st = fn(*args)
     if st != TTT_OK:
         check(st, name)
+
+
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream, t):
+    """What a call on a stream of its own allocates (outputs, workspace, turned Q and K) has to belong
+    to that stream: the current one's memory may be given away, or still be in use, while it runs."""
+    if stream is None:
+        return _CURRENT
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, a tensor on {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def ctypes_stream(s) -> int:
@@ -644,22 +658,24 @@ def ttt_rope(Q, K, rope, positions=None, first_position=0, inverse=False, Q_out=
         Hk = K.shape[1]
         if K.dtype != Q.dtype or K.shape[0] != B or tuple(K.shape[2:]) != (T, d):
             raise ValueError("K must have Q's type and shape but for the heads")
-        K_out = _out_as(K_out, (B, Hk, T, d), K, "K_out")
     elif K_out is not None:
         raise ValueError("K_out without K")
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")
     if positions is not None:
         _ints(positions, "positions", (B, T))
-    Q_out = _out_as(Q_out, (B, Hq, T, d), Q, "Q_out")
-    _same_device(Q, K, rope.inv_freq, positions, Q_out, K_out)
-    strides = ctypes.c_longlong * 3
-    sq = strides(*Q.stride()[:3])
-    sk = strides(*K.stride()[:3]) if K is not None else None
-    _call("ttt_rope", Q.device, _ptr(Q), _ptr(K), _QKV_DTYPES[Q.dtype], _ptr(positions), int(first_position),
-          _ptr(rope.inv_freq), rope.rotary, int(rope.interleaved), rope.mscale, int(bool(inverse)), B, Hq, Hk, T, d, sq,
-          sk, _ptr(Q_out), _ptr(K_out), _stream(stream, Q.device))
-    return Q_out, K_out
+    with _on(stream, Q):
+        Q_out = _out_as(Q_out, (B, Hq, T, d), Q, "Q_out")
+        if K is not None:
+            K_out = _out_as(K_out, (B, Hk, T, d), K, "K_out")
+        _same_device(Q, K, rope.inv_freq, positions, Q_out, K_out)
+        strides = ctypes.c_longlong * 3
+        sq = strides(*Q.stride()[:3])
+        sk = strides(*K.stride()[:3]) if K is not None else None
+        _call("ttt_rope", Q.device, _ptr(Q), _ptr(K), _QKV_DTYPES[Q.dtype], _ptr(positions), int(first_position),
+              _ptr(rope.inv_freq), rope.rotary, int(rope.interleaved), rope.mscale, int(bool(inverse)), B, Hq, Hk, T,
+              d, sq, sk, _ptr(Q_out), _ptr(K_out), _stream(stream, Q.device))
+        return Q_out, K_out
 
 
 def linear_attn_workspace_bytes(shape, backward=False) -> int:
@@ -697,17 +713,18 @@ def ttt_linear_attn_fwd(Q, K, V, log_decay, scale=None, S0=None, lengths=None, r
     K are turned first, at positions [B,T] int32 or t.  workspace: a uint8 CUDA tensor of
     linear_attn_workspace_bytes (allocated when None).  Returns (Z [B,H,T,d] in Q's type,
     S_out [B,H,d,d] f32, the state to continue from or to decode with)."""
-    if rope is not None:
-        Q, K = ttt_rope(Q, K, rope, positions=positions, stream=stream)
-    elif positions is not None:
-        raise ValueError("positions without a rope")
-    dt, (B, H, T, d), scale, workspace = _attn_args(Q, K, V, log_decay, scale, S0, lengths, workspace, False)
-    Z = _out_as(Z, (B, H, T, d), Q, "Z")
-    S_out = _out(S_out, (B, H, d, d), Q.device, "S_out")
-    _same_device(Q, Z, S_out)
-    _call("ttt_linear_attn_fwd", Q.device, _ptr(Q), _ptr(K), _ptr(V), dt, _ptr(log_decay), _ptr(S0), _ptr(lengths),
-          scale, B, H, T, d, _ptr(Z), _ptr(S_out), *_ws(workspace), _stream(stream, Q.device))
-    return Z, S_out
+    with _on(stream, Q):
+        if rope is not None:
+            Q, K = ttt_rope(Q, K, rope, positions=positions)
+        elif positions is not None:
+            raise ValueError("positions without a rope")
+        dt, (B, H, T, d), scale, workspace = _attn_args(Q, K, V, log_decay, scale, S0, lengths, workspace, False)
+        Z = _out_as(Z, (B, H, T, d), Q, "Z")
+        S_out = _out(S_out, (B, H, d, d), Q.device, "S_out")
+        _same_device(Q, Z, S_out)
+        _call("ttt_linear_attn_fwd", Q.device, _ptr(Q), _ptr(K), _ptr(V), dt, _ptr(log_decay), _ptr(S0), _ptr(lengths),
+              scale, B, H, T, d, _ptr(Z), _ptr(S_out), *_ws(workspace), _stream(stream, Q.device))
+        return Z, S_out
 
 
 def ttt_linear_attn_bwd(Q, K, V, log_decay, dZ, scale=None, S0=None, dS_T=None, lengths=None, rope=None,
@@ -716,25 +733,26 @@ def ttt_linear_attn_bwd(Q, K, V, log_decay, dZ, scale=None, S0=None, dS_T=None, 
     S_out>.  dZ [B,H,T,d] in Q's type, dS_T [B,H,d,d] f32 or None.  Returns a dict: dQ, dK, dV
     [B,H,T,d] in Q's type and dS0 [B,H,d,d] f32.  With a rope dQ and dK are those of the Q
     and K before the turn."""
-    if rope is not None:
-        Q, K = ttt_rope(Q, K, rope, positions=positions, stream=stream)
-    elif positions is not None:
-        raise ValueError("positions without a rope")
-    dt, (B, H, T, d), scale, workspace = _attn_args(Q, K, V, log_decay, scale, S0, lengths, workspace, True)
-    _cuda(dZ, "dZ", Q.dtype)
-    if dZ.shape != Q.shape:
-        raise ValueError(f"dZ must have shape {tuple(Q.shape)}, got {tuple(dZ.shape)}")
-    if dS_T is not None:
-        _shaped(dS_T, "dS_T", (B, H, d, d))
-    _same_device(Q, dZ, dS_T)
-    out = {n: torch.empty_like(Q) for n in ("dQ", "dK", "dV")}
-    out["dS0"] = torch.empty(B, H, d, d, device=Q.device)
-    _call("ttt_linear_attn_bwd", Q.device, _ptr(Q), _ptr(K), _ptr(V), dt, _ptr(log_decay), _ptr(S0), _ptr(lengths),
-          scale, _ptr(dZ), _ptr(dS_T), B, H, T, d, _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(out["dS0"]),
-          *_ws(workspace), _stream(stream, Q.device))
-    if rope is not None:
-        out["dQ"], out["dK"] = ttt_rope(out["dQ"], out["dK"], rope, positions=positions, inverse=True, stream=stream)
-    return out
+    with _on(stream, Q):
+        if rope is not None:
+            Q, K = ttt_rope(Q, K, rope, positions=positions)
+        elif positions is not None:
+            raise ValueError("positions without a rope")
+        dt, (B, H, T, d), scale, workspace = _attn_args(Q, K, V, log_decay, scale, S0, lengths, workspace, True)
+        _cuda(dZ, "dZ", Q.dtype)
+        if dZ.shape != Q.shape:
+            raise ValueError(f"dZ must have shape {tuple(Q.shape)}, got {tuple(dZ.shape)}")
+        if dS_T is not None:
+            _shaped(dS_T, "dS_T", (B, H, d, d))
+        _same_device(Q, dZ, dS_T)
+        out = {n: torch.empty_like(Q) for n in ("dQ", "dK", "dV")}
+        out["dS0"] = torch.empty(B, H, d, d, device=Q.device)
+        _call("ttt_linear_attn_bwd", Q.device, _ptr(Q), _ptr(K), _ptr(V), dt, _ptr(log_decay), _ptr(S0), _ptr(lengths),
+              scale, _ptr(dZ), _ptr(dS_T), B, H, T, d, _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(out["dS0"]),
+              *_ws(workspace), _stream(stream, Q.device))
+        if rope is not None:
+            out["dQ"], out["dK"] = ttt_rope(out["dQ"], out["dK"], rope, positions=positions, inverse=True)
+        return out
 
 
 def ttt_linear_attn_decode(q, k, v, log_decay, S, scale=None, rope=None, positions=None, z=None, stream=None):
@@ -756,14 +774,15 @@ def ttt_linear_attn_decode(q, k, v, log_decay, S, scale=None, rope=None, positio
         if not isinstance(rope, Rope):
             raise TypeError("rope must be a Rope")
         _ints(positions, "positions", (B,))
-    z = _out_as(z, (B, H, d), q, "z")
-    inv_freq = None if rope is None else rope.inv_freq
-    _same_device(q, k, v, log_decay, S, positions, inv_freq, z)
-    _call("ttt_linear_attn_decode", q.device, _ptr(q), _ptr(k), _ptr(v), _QKV_DTYPES[q.dtype], _ptr(log_decay),
-          float(d ** -0.5 if scale is None else scale), _ptr(S), _ptr(positions), _ptr(inv_freq),
-          0 if rope is None else rope.rotary, 0 if rope is None else int(rope.interleaved),
-          1.0 if rope is None else rope.mscale, B, H, d, _ptr(z), _stream(stream, q.device))
-    return z
+    with _on(stream, q):
+        z = _out_as(z, (B, H, d), q, "z")
+        inv_freq = None if rope is None else rope.inv_freq
+        _same_device(q, k, v, log_decay, S, positions, inv_freq, z)
+        _call("ttt_linear_attn_decode", q.device, _ptr(q), _ptr(k), _ptr(v), _QKV_DTYPES[q.dtype], _ptr(log_decay),
+              float(d ** -0.5 if scale is None else scale), _ptr(S), _ptr(positions), _ptr(inv_freq),
+              0 if rope is None else rope.rotary, 0 if rope is None else int(rope.interleaved),
+              1.0 if rope is None else rope.mscale, B, H, d, _ptr(z), _stream(stream, q.device))
+        return z
 
 
 def set_path(path: int) -> int:

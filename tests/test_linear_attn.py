@@ -332,6 +332,74 @@ def test_two_streams_at_once(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_stream_argument(dtype):
+    """A call on a stream of its own that is behind: what the call allocated for itself stays its own
+    while the current stream allocates and writes."""
+    c = make(1, 4, 2000, dtype, "slow", True, back=True)
+    x, plan = device(c, dtype), ttt.Rope.build(64)
+    assert ttt.linear_attn_workspace_bytes((1, 4, 2000, D)) > 0
+    want = {**run_fwd(x, rope=plan), **run_bwd(x, rope=plan)}
+    q, k, v = (x[n][:, :, 0].contiguous() for n in "QKV")
+    at = torch.tensor([5], dtype=torch.int32, device="cuda")
+    S_want = x["S0"].clone()
+    z_want = ttt.ttt_linear_attn_decode(q, k, v, x["log_decay"], S_want, rope=plan, positions=at)
+    S = x["S0"].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # ~10 ms
+    got = {**run_fwd(x, rope=plan, stream=side), **run_bwd(x, rope=plan, stream=side)}
+    z = ttt.ttt_linear_attn_decode(q, k, v, x["log_decay"], S, rope=plan, positions=at, stream=side)
+    waste = [torch.full((1 << n,), 0x40, dtype=torch.uint8, device="cuda") for n in range(9, 24) for _ in range(4)]
+    torch.cuda.current_stream().wait_stream(side)
+    assert len(waste) == 60 and torch.equal(z, z_want) and torch.equal(S, S_want)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+
+
+def test_states_handed_on_in_two_streams_and_graphs():
+    """More units than SMs: two calls at once and two graphs that replay side by side, each with the
+    workspace that it allocated."""
+    cs = [make(40, 5, 700, "bf16", "slow", True, back=True, seed=s) for s in (1, 2)]
+    xs = [device(c, "bf16") for c in cs]
+    want = [{**run_fwd(x), **run_bwd(x)} for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(3):
+        for i, (x, s) in enumerate(zip(xs, streams)):
+            with torch.cuda.stream(s):
+                got[i] = {**run_fwd(x), **run_bwd(x)}
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in xs], []
+    for x, g in zip(xs, graphs):
+        with torch.cuda.graph(g):
+            outs.append({**run_fwd(x), **run_bwd(x)})
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for results in (got, outs):
+        for g, w in zip(results, want):
+            for n in w:
+                assert torch.equal(g[n], w[n]), n
+    assert ttt.last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_thousands_of_short_sequences(dtype):
+    """Dozens of segments a CTA, of a chunk or none."""
+    lengths = [(7 * i) % 42 for i in range(1400)]
+    c = make(1400, 5, 41, dtype, "slow", lengths=lengths, back=True)
+    x = device(c, dtype)
+    for fn, run in (("fwd", run_fwd), ("bwd", run_bwd)):
+        ref = reference(c, fn)
+        check(run(x), ref, bounds(c, fn, dtype, ref))
+    assert ttt.last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_captured_and_replayed(dtype):
     c, c2 = (make(2, 2, 900, dtype, "slow", True, back=True, lengths=[900, 400], seed=s) for s in (1, 2))
     x, new = device(c, dtype), device(c2, dtype)
