@@ -307,12 +307,9 @@ __device__ __forceinline__ void attn_segment(const Params &p, int segment) {
       }
     }
     if (has_state) {
-      // C <- gamma^n C + e sum_s h_s y_s^T w_s.
-      const float dn = pw[n];
-#pragma unroll
-      for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) C[i][j] *= dn;
+      // C <- gamma^n C + e sum_s h_s y_s^T w_s.  The chunk's sum is one of its own: added token by token C
+      // would be rounded T times, not T / 64 times, which without decay costs digits (T = 32768: ~1e-6).
+      float M[ROWS][8] = {};
 #pragma unroll 2
       for (int s = 0; s < n; ++s) {
         const float h = p.e * pw[REVERSE ? s + 1 : n - 1 - s];
@@ -321,9 +318,14 @@ __device__ __forceinline__ void attn_segment(const Params &p, int segment) {
         for (int i = 0; i < ROWS; i += 4) {
           const float4 y = lds4(Ys + s * LD + state_row(i));
 #pragma unroll
-          for (int ii = 0; ii < 4; ++ii) row_times(C[i + ii], h * component(y, ii), u, v);
+          for (int ii = 0; ii < 4; ++ii) row_times(M[i + ii], h * component(y, ii), u, v);
         }
       }
+      const float dn = pw[n];
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) C[i][j] = fmaf(dn, C[i][j], M[i][j]);
     }
     __syncthreads();  // every read of the state and of the tiles is done
     if (!STATE_ONLY && half == 0) state_to(Cs, LD);

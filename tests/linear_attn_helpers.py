@@ -79,9 +79,10 @@ def bounds(c, fn, dtype, ref):
       value and its argument, rounded once, is off by |n g| half steps, which counts only where
       gamma^n >= e^-104 (fp32 holds nothing below): 104 + 4.  Together at most
       64 + 64 + 128 + 128 + 4 ceil(T / 64) + 2 (104 + 4) + 8 roundings.
-      bf16: the masked products are an operand in bf16 (one half step of bf16 times A), the
-      state is an operand as two bf16 numbers (at most U^2, times A), and the output is
-      rounded once (one half step times the value)."""
+      bf16: a summand of an output passes one operand rounded to bf16, the masked products or
+      the state (one half step of bf16 times A), and the output is rounded once (one half step
+      times the value).  The states themselves pass no rounding to bf16: the decayed rows that
+      enter them are three bf16 numbers, all of fp32."""
     A = _magnitude(c, fn)
     T = c["Q"].shape[2]
     n = 64 + 64 + 128 + 128 + 4 * -(-T // 64) + 2 * 108 + 8
@@ -90,11 +91,9 @@ def bounds(c, fn, dtype, ref):
         state = name in ("S", "dS0")
         b = n * U32 * a
         if dtype == "bf16":
-            # A state's summands have one operand, the decayed row, as two bf16 numbers.
-            b = b + U["bf16"] ** 2 * a
             if not state:
                 b = b + U["bf16"] * a + U["bf16"] * np.abs(ref[name]) * (1 + U["bf16"])
-                b = b + U["bf16"] ** 2 * a
+                b = b + U["bf16"] ** 2 * a  # both on one summand
         elif not state:
             b = b + U32 * np.abs(ref[name])
         # What underflows: gamma^n below the smallest fp32 value counts as zero.
