@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
     vb.get(fb);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (INTERLEAVED) {
+      if constexpr (INTERLEAVED) {
         constexpr int H = V / 2;
         if (a * H + i < half) {
           float &u = i < H ? fa[2 * (i % H)] : fb[2 * (i % H)], &w = i < H ? fa[2 * (i % H) + 1] : fb[2 * (i % H) + 1];

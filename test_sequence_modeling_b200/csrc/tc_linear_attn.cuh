@@ -8,7 +8,7 @@
 // One CTA of 24 warps an SM takes segments of units in turn (a CTA's roles run on into its next
 // segment without a stop); the roles run apart and meet at mbarriers:
 //   warp 0        TMA: x, y, w tiles of a chunk, two slots each, refilled one by one
-//   warp 1        issues every product: w^T y', x C, the next chunk's x y^T, P w
+//   warp 1        issues every product: w^T y', x C, P w, the next chunk's x y^T
 //   warp 3        says ahead which segments there are, with their powers of gamma
 //   warps 4-11    P: row t of 128 columns out of tensor memory (two warps a row), masked and
 //                 decayed, back as the bf16 A operand of P w
@@ -109,6 +109,14 @@ constexpr int OUT_ROWS = 32;                           // rows of an output stor
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// tmem_ld_16x256b_x8 over 2 groups of 8 columns (16 columns).
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(taddr));
 }
 
 // 3-D tiled store of a box out of shared memory (rows past the tensor's end are left out).
@@ -364,8 +372,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       return true;
     };
     Said g;
-    int total = 0;
-    for (int k = 0; segment(k, g); ++k) total += g.nchunks;
+    int total = 0;  // (a lane every 32nd segment: there may be thousands of a chunk each)
+    for (int k = lane; segment(k, g); k += 32) total += g.nchunks;
+    total = __reduce_add_sync(0xffffffffu, total);
     if (lane == 0) {
       *reinterpret_cast<int *>(sm + OFF_TOTAL) = total;
       mbar_arrive(&bars[SUM]);
@@ -604,7 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // (A state handed on lies as this kernel carries it, C^T.)
         const bool handed = work.steps && g.slot >= 0;
         if (handed && !(ok = wait_handed(work.ticket + 1 + g.slot, abort))) break;
-        const float *C0 = lattn::start_state(ps.p[g.pass], g.unit, handed ? g.slot : g.slot);
+        const float *C0 = lattn::start_state(ps.p[g.pass], g.unit, g.slot);
         const bool as_is = ps.p[g.pass].transposed || handed;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
