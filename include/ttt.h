@@ -408,13 +408,19 @@ TTT_API int ttt_mlp_momentum_decode(const void *q, const void *k, const void *v,
  * [B][H][d][d] fp32 or NULL: the state after each sequence's last token (S0, or
  * zero, for an empty one).
  * d = 64 (else TTT_ERR_UNSUPPORTED), any T >= 0; B*H*T*d < 2^40.  scale must be
- * finite.  Arithmetic: chunks of masked products.  With fp32 inputs fp32 FMAs.
+ * finite.  Arithmetic: chunks of masked products.  With bf16 inputs on the tensor
+ * cores (chunks of 128 tokens; each summand of Z passes one operand rounded to
+ * bf16, as coarse as Z's own rounding; the state stays fp32 throughout), unless
+ * ttt_set_path(TTT_PATH_SIMT); with fp32 inputs fp32 FMAs (chunks of 64).  A chunk's
+ * masked products multiply zeros with the later tokens of the chunk: a value there
+ * that is not finite may show in the rows of its chunk before it, too.
  *
  * workspace: DEVICE memory owned by the caller, 16-byte aligned, at least
  * ttt_linear_attn_workspace_bytes(B, H, T, d, 0) bytes (often 0, then NULL is
  * allowed): with few (batch, head) units a sequence is cut into segments whose
- * states lie there.  It needs no clearing; calls ordered on one stream may share
- * it, calls that may overlap (other streams, graphs that replay side by side) not.
+ * states lie there, with many the blocks that share a sequence hand its state on
+ * through it.  It needs no clearing; calls ordered on one stream may share it, calls
+ * that may overlap (other streams, graphs that replay side by side) not.
  * Errors as for the forward entry points; TTT_ERR_ARG also for a scale that is not
  * finite and a workspace that is null or too small.
  */
@@ -436,7 +442,7 @@ TTT_API size_t ttt_linear_attn_workspace_bytes(int B, int H, int T, int d, int b
  * fp32 or NULL (zero).  Outputs: dQ, dK, dV [B][H][T][d] in the type of Q, K, V,
  * rounded once from fp32, zeros behind the ends; dS0 [B][H][d][d] fp32 or NULL
  * (dS_T for an empty sequence).  The states are recomputed from Q, K, V: nothing of
- * the forward is kept.  workspace as for the forward (backward = 1).
+ * the forward is kept.  Arithmetic and workspace as for the forward (backward = 1).
  */
 TTT_API int ttt_linear_attn_bwd(const void *Q, const void *K, const void *V, int qkv_dtype,
                                 const float *log_decay, const float *S0, const int *lengths,
@@ -501,7 +507,8 @@ TTT_API int ttt_last_device_status(void *stream);
  * kernels for every case) or TTT_PATH_TC (tensor cores; calls outside the
  * tensor-core sizes return TTT_ERR_UNSUPPORTED).  It applies to the entry points
  * that have a tensor-core kernel: ttt_linear_fwd, ttt_linear_ln_fwd, ttt_mlp_fwd
- * (and ttt_fwd_host) and ttt_linear_momentum_fwd / ttt_linear_ln_momentum_fwd;
+ * (and ttt_fwd_host), ttt_linear_momentum_fwd / ttt_linear_ln_momentum_fwd, and
+ * ttt_linear_attn_fwd / ttt_linear_attn_bwd (tensor cores: bf16 inputs, any T);
  * the others run their CUDA-core kernels under every path.  Returns the previous
  * path, or TTT_ERR_ARG for an unknown value.
  */

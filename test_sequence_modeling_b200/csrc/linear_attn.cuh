@@ -173,7 +173,8 @@ constexpr size_t SMEM_BYTES = sizeof(float) * (size_t)(5 * CHUNK * LD + 2 * CHUN
 // an 8 x 8 register tile of one 64 x 64 product each: the first takes m o (x y^T) and then the state's
 // y^T w, the second x C and then (m o x y^T) w on top of it, so that each does as much.  8 x 8, because with
 // 4 x 4 tiles and 256 threads the operands' reads from shared memory took twice the arithmetic's time:
-// forward B6 H8 T1999 145 us, against 121 now, of which the arithmetic is about half.
+// forward B6 H8 T1999 145 us, against 124 now, of which the arithmetic is about half.  B16 H12 T2048 436 us
+// (26 TFLOP/s without the quarters left out, 35 % of the CUDA cores' 74), backward 863 us.
 template <typename InT, bool REVERSE, bool STATE_ONLY>
 __device__ __forceinline__ void attn_segment(const Params &p, int segment) {
   extern __shared__ __align__(16) float sm[];
@@ -402,7 +403,8 @@ __global__ void __launch_bounds__(SCAN_THREADS) scan_kernel(const ScanParams p) 
 // One token of every unit: S <- gamma S + k^T v, z = scale q S, with q and k turned by the
 // token's position first when a rotary plan is given.  One CTA a unit: each thread takes four
 // float4 of the state (rows ty + 16 i, columns 4 tx ..), all loaded before anything waits.
-// 32 KB of state move a unit against 16 KFLOP: bound by memory.
+// 32 KB of state move a unit against 16 KFLOP: bound by memory (B512 H32: 85 us, 6.4 TB/s, 98 % of
+// the measured copy; B1 H32: 3.1 us, a launch).
 struct DecodeParams {
   const void *q, *k, *v;   // [units][D]
   const float *log_decay;  // [H]

@@ -122,7 +122,7 @@ struct Piece<__nv_bfloat16, 1> {
 
 // A thread takes two pieces of V values of a row.  Half layout: a piece and its partner, V the most
 // values up to 16 bytes that rotary / 2 is a multiple of (a narrower piece costs more instructions:
-// bf16, B16 H32 T2048: 87 us at V = 8; see ttt_rope's choice).  Interleaved: two neighbouring pieces of 16
+// bf16, B16 H32 T2048: 87 us at V = 8, 6.2 TB/s, 94 % of the measured copy; 92 us at V = 4, rotary 40).  Interleaved: two neighbouring pieces of 16
 // bytes, whose pairs are inside.
 template <typename InT, int V, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
