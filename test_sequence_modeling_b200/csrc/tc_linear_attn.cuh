@@ -34,7 +34,7 @@
 // Measured on one B200 at 1965 MHz: forward B16 H32 T8192 411 us (2.16 GB: 5.2 TB/s, 80 % of the
 // measured copy), B16 H12 T2048 55 us (3.7 TB/s), B1 H32 T32768, which is cut, 184 us (0.54 GB, and
 // 0.24 GB again for the segments' states: 4.2 TB/s); backward of the latter two 135 us (three passes of
-// four tensors, 0.6 GB: 4.5 TB/s) and 425 us (1.6 GB by 96 CTAs, a unit of a pass each: 3.8 TB/s).  A
+// four tensors, 0.6 GB: 4.5 TB/s) and 425 us (cut in three; 1.6 GB, and 0.36 GB again: 4.6 TB/s).  A
 // launch's start and end cost about 10 us.  Called without a pause for seconds the kernel reaches the board's power limit (1000 W; a
 // plain copy takes 550), the clock falls to 1.5 GHz, and the first takes 480 to 510 us.  A chunk takes
 // 3650 cycles: the products one after the other with what they wait for.  What did not help, all measured:

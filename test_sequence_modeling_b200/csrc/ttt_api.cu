@@ -753,7 +753,7 @@ int check_buffers(std::initializer_list<Buffer> ins, std::initializer_list<Buffe
 // the two more launches 4 (0.4, of a step that is ten times as long); two segments an SM at a time, which
 // only the CUDA-core kernel takes, 1.6 times as long as one, more of them 0.8 of their number and a bit.
 // Forward and backward, us, for 1 to 32 segments a unit:
-//   bf16 B1 H32 T32768  1: 421, 4: 189, 9: 181 (taken), 18: 196      1: 445, 4: 488, 9: 469
+//   bf16 B1 H32 T32768  1: 421, 4: 189, 9: 181 (taken), 18: 196      1: 445, 3: 425 (taken), 4: 488, 9: 469
 //   bf16 B1 H12 T4096   1: 59, 4: 37, 8: 27, 12: 27, 24: 32          1: 63, 4: 40 (taken), 8: 45, 16: 52
 //   fp32 B6 H8 T1999    1: 266, 4: 158, 6: 124 (taken), 8: 161       1: 265 (taken), 2: 302, 6: 322
 //   fp32 B3 H5 T777     1: 105, 2: 97, 4: 53, 7: 32 (taken)          1: 109, 4: 76, 7: 56 (taken)
