@@ -534,11 +534,10 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
             }
           }
-          // The last chunk's P w has read what this overwrites.
-          if (i > 0 && j == 2 * half && !(ok = wait_warp(&bars[OFULL], (uint32_t)(i - 1) & 1u, abort))) break;
+          // The last chunk's P w has read what this overwrites: it was issued before this chunk's P, and the
+          // barrier of that stands for all products issued before.
           tmem_st_32x32b_x16(dst + 16 * j, pk);
         }
-        if (!ok) break;
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -703,6 +702,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_wait_ld();
           loaded(xc);
           loaded(pv);
+          if (h == 3) {  // the products' places are free
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[OFREE]);
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float2 v =
@@ -717,11 +721,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           *reinterpret_cast<uint4 *>(sm + OFF_OUT + sw128_offset(t, 16 * h)) = make_uint4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<uint4 *>(sm + OFF_OUT + sw128_offset(t, 16 * h + 8)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        tc_fence_before_sync();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bars[OFREE]);
           const int t0 = g.t_lo + c0 + 32 * w4;
           if (t0 < p.T) tma_store_3d(&maps.pass[g.pass].out, sm + OFF_OUT + 32 * w4 * 128, 0, t0, g.unit);
         }
