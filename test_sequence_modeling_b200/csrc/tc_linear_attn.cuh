@@ -31,16 +31,16 @@
 // own.  Their loops are kept short: with the loops unrolled the five roles missed the instruction
 // cache and the same kernel took 1.5 times as long.
 //
-// Measured on one B200 at 1965 MHz: forward B16 H32 T8192 411 us (2.16 GB: 5.2 TB/s, 80 % of the
-// measured copy), B16 H12 T2048 55 us (3.7 TB/s), B1 H32 T32768, which is cut, 184 us (0.54 GB, and
-// 0.24 GB again for the segments' states: 4.2 TB/s); backward of the latter two 135 us (three passes of
-// four tensors, 0.6 GB: 4.5 TB/s) and 425 us (cut in three; 1.6 GB, and 0.36 GB again: 4.6 TB/s).  A
+// Measured on one B200 at 1965 MHz: forward B16 H32 T8192 402 us (2.16 GB: 5.4 TB/s, 82 % of the
+// measured copy), B16 H12 T2048 53 us (3.8 TB/s), B1 H32 T32768, which is cut, 180 us (0.54 GB, and
+// 0.24 GB again for the segments' states: 4.3 TB/s); backward of the latter two 132 us (three passes of
+// four tensors, 0.6 GB: 4.6 TB/s) and 405 us (cut in three; 1.6 GB, and 0.36 GB again: 4.9 TB/s).  A
 // launch's start and end cost about 10 us.  Called without a pause for seconds the kernel reaches the board's power limit (1000 W; a
-// plain copy takes 550), the clock falls to 1.5 GHz, and the first takes 480 to 510 us.  A chunk takes
-// 3650 cycles: the products one after the other with what they wait for.  What did not help, all measured:
-// three slots for the tiles at the price of one buffer for y' (444 us), a second P in tensor memory, so
-// that the next chunk's is there early, at the price of a state product in 64 columns (457), 28 warps with
-// two that issue (490 against 450 then), a prefetch of the next tiles to L2, y' unrolled.
+// plain copy takes 550), the clock falls to 1.5 GHz, and the first takes 480 to 500 us.  A chunk takes
+// 3570 cycles: the products one after the other with what they wait for.  What did not help, all measured:
+// three slots for the tiles at the price of one buffer for y' (444 us, 425 then), a second P in tensor
+// memory, so that the next chunk's is there early, at the price of a state product in 64 columns (457), 28
+// warps with two that issue, a prefetch of the next tiles to L2, y' unrolled.
 //
 // Precision: x, y, w are exact in bf16 and every product accumulates in fp32.  Each summand of
 // an output passes one operand rounded to bf16, P o m or C (2^-8 of it, as coarse as the
@@ -165,9 +165,10 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
   return mbar_try_wait(bar, parity) || wait_longer(bar, parity, abort, limit);
 }
 
-// The same for a whole warp, one answer for all lanes.
+// The same for a whole warp, one answer for all lanes.  (Mostly the turn is over: one try and one vote.)
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  return __all_sync(0xffffffffu, wait(bar, parity, abort));
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_longer(bar, parity, abort, WAIT_LIMIT));
 }
 
 // x less a pair of bf16 numbers, exact for the numbers nearest to x.
