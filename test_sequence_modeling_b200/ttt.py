@@ -51,9 +51,14 @@ def _qkv(Q, K, V):
     return _QKV_DTYPES[Q.dtype]
 
 
+def _f32(device, *shape):
+    """A buffer for what the library writes in fp32, whatever torch's default type is."""
+    return torch.empty(shape, dtype=torch.float32, device=device)
+
+
 def _out(t, shape, device, name):
     if t is None:
-        return torch.empty(shape, dtype=torch.float32, device=device)
+        return _f32(device, *shape)
     _cuda(t, name, torch.float32)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}")
@@ -279,13 +284,13 @@ def ttt_linear_bwd(Q, K, V, eta, W0, dZ, b, dW_T=None, gamma=None, beta=None, ep
     if b <= 0 or T % b:
         raise ValueError("T must be a multiple of b")
     dev = Q.device
-    out = {n: torch.empty(B, H, T, d, device=dev) for n in ("dQ", "dK", "dV")}
-    out["deta"] = torch.empty(B, H, T, device=dev)
-    out["dW0"] = torch.empty(B, H, d, d, device=dev)
-    out["W_ckpt"] = torch.empty(B, H, T // b, d, d, device=dev)
+    out = {n: _f32(dev, B, H, T, d) for n in ("dQ", "dK", "dV")}
+    out["deta"] = _f32(dev, B, H, T)
+    out["dW0"] = _f32(dev, B, H, d, d)
+    out["W_ckpt"] = _f32(dev, B, H, T // b, d, d)
     if ln:
-        out["dgamma"] = torch.empty(B, H, d, device=dev)
-        out["dbeta"] = torch.empty(B, H, d, device=dev)
+        out["dgamma"] = _f32(dev, B, H, d)
+        out["dbeta"] = _f32(dev, B, H, d)
     o = {k: _ptr(v) for k, v in out.items()}
     dwt = _ptr(dW_T)
     with torch.cuda.device(dev):
@@ -316,9 +321,9 @@ def ttt_mlp_momentum_fwd(Q, K, V, eta, alpha, lam, W1, W2, gamma, beta, b, eps=1
     for n, t in (("gamma", gamma), ("beta", beta)):
         _shaped(t, n, (H, d))
     dev = Q.device
-    Z = torch.empty(B, H, T, d, device=dev)
-    W1o, S1o = (torch.empty(B, H, d, h, device=dev) for _ in range(2))
-    W2o, S2o = (torch.empty(B, H, h, d, device=dev) for _ in range(2))
+    Z = _f32(dev, B, H, T, d)
+    W1o, S1o = (_f32(dev, B, H, d, h) for _ in range(2))
+    W2o, S2o = (_f32(dev, B, H, h, d) for _ in range(2))
     with torch.cuda.device(dev):
         st = _lib.load().ttt_mlp_momentum_fwd(
             _ptr(Q), _ptr(K), _ptr(V), dt, _ptr(eta), _ptr(alpha), _ptr(lam), _ptr(W1), _ptr(W2),
@@ -349,14 +354,14 @@ def ttt_mlp_bwd(Q, K, V, eta, W1, W2, gamma, beta, dZ, b, eps=1e-6, dW1_T=None, 
     if b <= 0 or T % b:
         raise ValueError("T must be a multiple of b")
     dev = Q.device
-    out = {n: torch.empty(B, H, T, d, device=dev) for n in ("dQ", "dK", "dV")}
-    out["deta"] = torch.empty(B, H, T, device=dev)
-    out["dW1"] = torch.empty(B, H, d, h, device=dev)
-    out["dW2"] = torch.empty(B, H, h, d, device=dev)
-    out["dgamma"] = torch.empty(B, H, d, device=dev)
-    out["dbeta"] = torch.empty(B, H, d, device=dev)
-    out["W1_ckpt"] = torch.empty(B, H, T // b, d, h, device=dev)
-    out["W2_ckpt"] = torch.empty(B, H, T // b, h, d, device=dev)
+    out = {n: _f32(dev, B, H, T, d) for n in ("dQ", "dK", "dV")}
+    out["deta"] = _f32(dev, B, H, T)
+    out["dW1"] = _f32(dev, B, H, d, h)
+    out["dW2"] = _f32(dev, B, H, h, d)
+    out["dgamma"] = _f32(dev, B, H, d)
+    out["dbeta"] = _f32(dev, B, H, d)
+    out["W1_ckpt"] = _f32(dev, B, H, T // b, d, h)
+    out["W2_ckpt"] = _f32(dev, B, H, T // b, h, d)
     o = {k: _ptr(v) for k, v in out.items()}
     with torch.cuda.device(dev):
         st = _lib.load().ttt_mlp_bwd(
@@ -746,7 +751,7 @@ def ttt_linear_attn_bwd(Q, K, V, log_decay, dZ, scale=None, S0=None, dS_T=None, 
             _shaped(dS_T, "dS_T", (B, H, d, d))
         _same_device(Q, dZ, dS_T)
         out = {n: torch.empty_like(Q) for n in ("dQ", "dK", "dV")}
-        out["dS0"] = torch.empty(B, H, d, d, device=Q.device)
+        out["dS0"] = _f32(Q.device, B, H, d, d)
         _call("ttt_linear_attn_bwd", Q.device, _ptr(Q), _ptr(K), _ptr(V), dt, _ptr(log_decay), _ptr(S0), _ptr(lengths),
               scale, _ptr(dZ), _ptr(dS_T), B, H, T, d, _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(out["dS0"]),
               *_ws(workspace), _stream(stream, Q.device))
