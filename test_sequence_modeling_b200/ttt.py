@@ -620,6 +620,14 @@ def _ints(t, name, shape):
     return t
 
 
+def _int32(x, name):
+    """x as the C int that the library takes; ctypes would wrap one that does not fit."""
+    v = int(x)
+    if v != x or not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} must be a whole number of 32 bits, got {x}")
+    return v
+
+
 def _same_device(Q, *tensors):
     """The C ABI reads plain pointers of one device."""
     device = Q.device
@@ -653,7 +661,7 @@ def _rope_rows(t, name):
 def ttt_rope(Q, K, rope, positions=None, first_position=0, inverse=False, Q_out=None, K_out=None, stream=None):
     """Rotary positions on Q [B,Hq,T,d] and K [B,Hk,T,d] (K may be None), f32 or bf16, at any
     strides with contiguous rows (see include/ttt.h).  positions [B,T] int32, or None:
-    first_position + t.  inverse: the turn back, which is the forward's gradient.  Returns
+    first_position + t, all within int32.  inverse: the turn back, which is the forward's gradient.  Returns
     (Q_out, K_out), dense [B,H,T,d] in the inputs' type (K_out None without K)."""
     _rope_rows(Q, "Q")
     B, Hq, T, d = Q.shape
@@ -667,6 +675,7 @@ def ttt_rope(Q, K, rope, positions=None, first_position=0, inverse=False, Q_out=
         raise ValueError("K_out without K")
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")
+    first = _int32(first_position, "first_position")
     if positions is not None:
         _ints(positions, "positions", (B, T))
     with _on(stream, Q):
@@ -677,7 +686,7 @@ def ttt_rope(Q, K, rope, positions=None, first_position=0, inverse=False, Q_out=
         strides = ctypes.c_longlong * 3
         sq = strides(*Q.stride()[:3])
         sk = strides(*K.stride()[:3]) if K is not None else None
-        _call("ttt_rope", Q.device, _ptr(Q), _ptr(K), _QKV_DTYPES[Q.dtype], _ptr(positions), int(first_position),
+        _call("ttt_rope", Q.device, _ptr(Q), _ptr(K), _QKV_DTYPES[Q.dtype], _ptr(positions), first,
               _ptr(rope.inv_freq), rope.rotary, int(rope.interleaved), rope.mscale, int(bool(inverse)), B, Hq, Hk, T,
               d, sq, sk, _ptr(Q_out), _ptr(K_out), _stream(stream, Q.device))
         return Q_out, K_out
