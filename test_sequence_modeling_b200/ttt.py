@@ -608,6 +608,8 @@ def rope_frequencies(rotary, base=10000.0, scaling=None, factor=1.0, original_le
         low = max(math.floor(pair_of(beta_fast)), 0)
         high = min(math.ceil(pair_of(beta_slow)), rotary - 1)
         slow = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+        if pair_of(beta_slow) < 0.0:  # the ramp ends before pair 0, where low is cut off: every pair is a slow one
+            slow = torch.ones_like(i)
         return (f / factor * slow + f * (1.0 - slow)).float(), 0.1 * math.log(factor) + 1.0
     raise ValueError(f"unknown scaling {scaling!r}: None, 'linear', 'ntk' or 'yarn'")
 
