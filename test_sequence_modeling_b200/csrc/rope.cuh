@@ -8,8 +8,9 @@
 // same mscale is the transpose, so it is the gradient's way back.
 //
 // The angle of a far position loses its digits in fp32 (at position 10^6 a step of the product is
-// 0.06 rad), so the product and its reduction to one turn are in fp64 and only the reduced angle
-// goes through sincosf, its rounding carried to first order.  A token's 32 angles serve all its
+// 0.06 rad), so the product and its reduction to one turn are in fp64, the product's own rounding
+// (from position 2^29 on) carried beside it, and only the reduced angle goes through sincosf, its
+// rounding carried to first order.  A token's 32 angles serve all its
 // heads of Q and K: a CTA makes them once for a tile of tokens.  Bound by memory: each row is read
 // and written once.
 #pragma once
@@ -33,10 +34,11 @@ struct Plan {
 
 // (cos, sin) of position x frequency, times mscale.
 __device__ __forceinline__ float2 cos_sin(int position, float inv_freq, float mscale) {
-  const double a = (double)position * (double)inv_freq;
+  const double p = position, f = inv_freq, a = p * f;
+  const double beyond = fma(p, f, -a);                         // what a's rounding left out (31 x 24 bits), exact
   const double turns = rint(a * 0.15915494309189535);          // 1 / (2 pi)
   double r = fma(turns, -6.283185307179586, a);                // 2 pi, high part
-  r = fma(turns, -2.4492935982947064e-16, r);                  // and the rest of it
+  r = fma(turns, -2.4492935982947064e-16, r + beyond);         // and the rest of it
   const float x = (float)r, rest = (float)(r - (double)x);
   float s, c;
   sincosf(x, &s, &c);
