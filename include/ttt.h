@@ -413,7 +413,9 @@ TTT_API int ttt_mlp_momentum_decode(const void *q, const void *k, const void *v,
  * bf16, as coarse as Z's own rounding; the state stays fp32 throughout), unless
  * ttt_set_path(TTT_PATH_SIMT); with fp32 inputs fp32 FMAs (chunks of 64).  A chunk's
  * masked products multiply zeros with the later tokens of the chunk: a value there
- * that is not finite may show in the rows of its chunk before it, too.
+ * that is not finite may show in the rows of its chunk before it, too.  What depends
+ * on a value that is not finite is not finite: an infinity of K or V is one in the
+ * state, and NaN once a power of gamma that fp32 holds as zero meets it.
  *
  * workspace: DEVICE memory owned by the caller, 16-byte aligned, at least
  * ttt_linear_attn_workspace_bytes(B, H, T, d, 0) bytes (often 0, then NULL is

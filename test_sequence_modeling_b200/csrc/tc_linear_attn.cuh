@@ -46,12 +46,14 @@
 // an output passes one operand rounded to bf16, P o m or C (2^-8 of it, as coarse as the
 // output's own rounding).  The state is an fp32 result that is carried on: it stays in fp32
 // registers, and the decayed rows y' that enter it are three bf16 numbers, all of fp32 (two
-// would leave 2.5e-6 of the state).
+// would leave 2.5e-6 of the state), cut off rather than rounded, so that an infinity's parts agree.
 #pragma once
 
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <cfloat>
 
 #include "device_status.cuh"
 #include "linear_attn.cuh"
@@ -171,7 +173,11 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, wait_longer(bar, parity, abort, WAIT_LIMIT));
 }
 
-// x less a pair of bf16 numbers, exact for the numbers nearest to x.
+// A pair's leading bits as bf16, cut off: three such parts hold all 24 bits, and all have the value's sign.
+__device__ __forceinline__ uint32_t leading_bf16x2(float2 x) {
+  return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+// x less a pair of bf16 numbers, exact for x's leading bits.
 __device__ __forceinline__ float2 minus_bf16x2(float2 x, uint32_t b) {
   float2 d;
   asm("{\n\t.reg .b16 lo, hi, m;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
@@ -591,7 +597,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             float2 r = __fmul2_rn(h, unpack_bf16x2(u[e]));
 #pragma unroll
             for (int m = 0; m < 3; ++m) {
-              part[m][e] = pack_bf16x2(r.x, r.y);
+              part[m][e] = leading_bf16x2(r);
               if (m < 2) r = minus_bf16x2(r, part[m][e]);
             }
           }
@@ -661,8 +667,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             auto pair = [&](int q) { return make_float2(__uint_as_float(m[q][e]), __uint_as_float(m[q][e + 1])); };
+            // Where an infinity of y or w makes the first part's sum infinite, the others' are infinities of its
+            // sign or NaN (inf - inf, 0 inf): min makes a finite number of both but for -inf, which agrees.  (A
+            // select of the finite ones instead: 1 to 2 % of the kernel's time, against 0.3 to 1 %.)
+            float2 rest = __fadd2_rn(pair(1), pair(2));
+            rest.x = fminf(rest.x, FLT_MAX);
+            rest.y = fminf(rest.y, FLT_MAX);
             const float2 v = __ffma2_rn(make_float2(dn, dn), make_float2(C[8 * h + e], C[8 * h + e + 1]),
-                                        __fadd2_rn(pair(0), __fadd2_rn(pair(1), pair(2))));
+                                        __fadd2_rn(pair(0), rest));
             C[8 * h + e] = v.x;
             C[8 * h + e + 1] = v.y;
           }
