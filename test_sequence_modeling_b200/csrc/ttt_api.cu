@@ -752,11 +752,18 @@ int check_buffers(std::initializer_list<Buffer> ins, std::initializer_list<Buffe
 // one B200: a state pass's step takes 0.65 of a full one (CUDA cores 0.5), a segment's start and end 0.7,
 // the two more launches 4 (0.4, of a step that is ten times as long); two segments an SM at a time, which
 // only the CUDA-core kernel takes, 1.6 times as long as one, more of them 0.8 of their number and a bit.
+// A cut has to gain 5 % by that count, which is no better than that: of 14 sizes with a lesser gain 12 took 2 to
+// 26 % longer cut (bf16 B1 H64 T4096 forward 64 against 60 whole, H28 T8192 backward 126 against 114, fp32 H111
+// T8192 forward 1152 against 1060; the other way fp32 H60 T777, 91 against 109, and H41 T8192, 3 %).
 // Forward and backward, us, for 1 to 32 segments a unit:
 //   bf16 B1 H32 T32768  1: 421, 4: 189, 9: 181 (taken), 18: 196      1: 445, 3: 425 (taken), 4: 488, 9: 469
+//   bf16 B1 H32 T8192   1: 105, 2: 104, 4: 64 (taken), 8: 69         1: 117 (taken), 2: 163, 3: 125, 4: 144
 //   bf16 B1 H12 T4096   1: 59, 4: 37, 8: 27, 12: 27, 24: 32          1: 63, 4: 40 (taken), 8: 45, 16: 52
 //   fp32 B6 H8 T1999    1: 266, 4: 158, 6: 124 (taken), 8: 161       1: 265 (taken), 2: 302, 6: 322
 //   fp32 B3 H5 T777     1: 105, 2: 97, 4: 53, 7: 32 (taken)          1: 109, 4: 76, 7: 56 (taken)
+// Equal cuts of all units do not help 75 to 147 units of a bf16 forward (or 38 to 49 of a backward): a second
+// round costs more than the idle SMs, and a CTA takes a unit, whatever their number (forward, us):
+//   bf16 B8 H12 T2048   1: 34 (taken), 2: 60, 4: 58        bf16 B8 H12 T8192   1: 109 (taken), 2: 159, 4: 143
 struct AttnPlan {
   lattn::Cut cut;
   int steps;            // > 0: the CTAs share the chunks
@@ -784,12 +791,12 @@ AttnPlan attn_plan(long long units, int T, bool backward, bool tensor_cores) {
   }
   const long long left = tensor_cores ? units : units % most;
   if (left == 0) return best;
-  const double state_step = tensor_cores ? 0.65 : 0.5, ends = 0.7, cut_steps = tensor_cores ? 4 : 0.4;
+  const double state_step = tensor_cores ? 0.65 : 0.5, ends = 0.7, cut_steps = tensor_cores ? 4 : 0.4, worth = 0.95;
   auto rounds = [&](long long n) {
     const long long r = (n + ATTN_SMS - 1) / ATTN_SMS;
     return tensor_cores || r < 2 ? (double)r : r == 2 ? 1.6 : 0.8 * ((double)n / ATTN_SMS + 0.35);
   };
-  double least = rounds(passes * left) * (chunks + ends);
+  double least = worth * rounds(passes * left) * (chunks + ends);
   for (int n = 2; n <= ATTN_MOST_SEGMENTS && n <= chunks; ++n) {
     const long long len = (chunks + n - 1) / n, nseg = (chunks + len - 1) / len;
     if (nseg != n) continue;

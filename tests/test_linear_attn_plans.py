@@ -13,8 +13,8 @@ from test_sequence_modeling_b200 import _lib as L
 pytestmark = pytest.mark.gpu
 
 # B, H, T and, for bf16, the launches of a forward and of a backward: 3 where the sequences are cut.
-PLANS = {"whole": (1, 3, 70, 1, 1), "cut": (2, 2, 1500, 3, 3), "cut, segments of two chunks": (7, 2, 1300, 3, 3),
-         "shared": (5, 30, 130, 1, 1), "shared, ragged": (4, 40, 300, 1, 1), "backward shared": (6, 10, 300, 1, 1)}
+PLANS = {"whole": (1, 3, 70, 1, 1), "cut": (2, 2, 1500, 3, 3), "cut, segments of two chunks": (5, 2, 1900, 3, 3),
+         "shared": (5, 30, 130, 1, 1), "shared, ragged": (6, 25, 200, 1, 1), "backward shared": (6, 9, 300, 1, 1)}
 
 
 def run_fwd(x, **kw):
@@ -45,6 +45,16 @@ def test_launches(plan):
     B, H, T, fwd, bwd = PLANS[plan]
     x = device(make(B, H, T, "bf16", back=True), "bf16")
     for run, want in ((run_fwd, fwd), (run_bwd, bwd)):
+        before = ttt.launch_count()
+        run(x)
+        assert ttt.launch_count() - before == want
+
+
+def test_a_cut_that_gains_nothing_is_not_taken():
+    """32 units of 64 chunks: the forward is cut (64 us against 105), the backward, 117 us whole and 125 in
+    three, is not."""
+    x = device(make(1, 32, 8192, "bf16", back=True), "bf16")
+    for run, want in ((run_fwd, 3), (run_bwd, 1)):
         before = ttt.launch_count()
         run(x)
         assert ttt.launch_count() - before == want
@@ -236,7 +246,7 @@ def _sums(x, y, w, alive, reverse):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("size", [(1, 32, 32768), (1, 3, 5000), (16, 12, 2048), (40, 5, 1000), (9, 1, 20000)], ids=str)
+@pytest.mark.parametrize("size", [(1, 9, 32768), (1, 3, 5000), (16, 12, 2048), (40, 5, 1000), (9, 1, 9000)], ids=str)
 @pytest.mark.parametrize("padded", [False, True])
 def test_whole_numbers_exactly(dtype, size, padded):
     """Undecayed sequences of one-hot rows: every product and sum is a whole number that bf16 holds exactly
