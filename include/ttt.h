@@ -410,8 +410,9 @@ TTT_API int ttt_mlp_momentum_decode(const void *q, const void *k, const void *v,
  * d = 64 (else TTT_ERR_UNSUPPORTED), any T >= 0; B*H*T*d < 2^40.  scale must be
  * finite.  Arithmetic: chunks of masked products.  With bf16 inputs on the tensor
  * cores (chunks of 128 tokens; each summand of Z passes one operand rounded to
- * bf16, as coarse as Z's own rounding; the state stays fp32 throughout), unless
- * ttt_set_path(TTT_PATH_SIMT); with fp32 inputs fp32 FMAs (chunks of 64).  A chunk's
+ * bf16, a product or the state, S0 included: as coarse as Z's own rounding, and with
+ * it 1.4 times its error; the state itself stays fp32 throughout), unless
+ * ttt_set_path(TTT_PATH_SIMT), which rounds Z alone, in several times the time; with fp32 inputs fp32 FMAs (chunks of 64).  A chunk's
  * masked products multiply zeros with the later tokens of the chunk: a value there
  * that is not finite may show in the rows of its chunk before it, too.  What depends
  * on a value that is not finite is not finite: an infinity of K or V is one in the

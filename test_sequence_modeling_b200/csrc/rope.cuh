@@ -10,9 +10,8 @@
 // The angle of a far position loses its digits in fp32 (at position 10^6 a step of the product is
 // 0.06 rad), so the product and its reduction to one turn are in fp64, the product's own rounding
 // (from position 2^29 on) carried beside it, and only the reduced angle goes through sincosf, its
-// rounding carried to first order.  A token's 32 angles serve all its
-// heads of Q and K: a CTA makes them once for a tile of tokens.  Bound by memory: each row is read
-// and written once.
+// rounding carried to first order.  A token's 32 angles serve all its heads of Q and K: a CTA makes
+// them once for a tile of tokens.  Bound by memory: each row is read and written once.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -124,8 +123,8 @@ struct Piece<__nv_bfloat16, 1> {
 
 // A thread takes two pieces of V values of a row.  Half layout: a piece and its partner, V the most
 // values up to 16 bytes that rotary / 2 is a multiple of (a narrower piece costs more instructions:
-// bf16, B16 H32 T2048: 87 us at V = 8, 6.2 TB/s, 94 % of the measured copy; 92 us at V = 4, rotary 40).  Interleaved: two neighbouring pieces of 16
-// bytes, whose pairs are inside.
+// bf16, B16 H32 T2048: 87 us at V = 8, 6.2 TB/s, 94 % of the measured copy; 92 us at V = 4, rotary 40).
+// Interleaved: two neighbouring pieces of 16 bytes, whose pairs are inside.
 template <typename InT, int V, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
   constexpr int ITEMS = D / V / 2;       // threads a row

@@ -24,27 +24,30 @@
 // comes last, when the CTA before it has handed its state on long ago.  A CTA's number is a ticket
 // taken at its start, so the one before it has started, and what it waits for waits for nothing.
 //
-// Why so: a chunk's 64 KB of HBM traffic take an SM 2860 cycles at the measured copy rate.  The
+// Why so: a chunk's 64 KB of HBM traffic take an SM 2920 cycles at the measured copy rate.  The
 // products take 1580 of them: measured back to back, a product with K = 16 takes N / 2 cycles for
 // N >= 128 whatever M is, and for N = 64 37 cycles with M = 64 or A in tensor memory, 52 else.  The
 // rest is the warps' work on what is between the products, so every part of it has warps of its
 // own.  Their loops are kept short: with the loops unrolled the five roles missed the instruction
 // cache and the same kernel took 1.5 times as long.
 //
-// Measured on one B200 at 1965 MHz: forward B16 H32 T8192 402 us (2.16 GB: 5.4 TB/s, 82 % of the
-// measured copy), B16 H12 T2048 53 us (3.8 TB/s), B1 H32 T32768, which is cut, 180 us (0.54 GB, and
-// 0.24 GB again for the segments' states: 4.3 TB/s); backward of the latter two 132 us (three passes of
-// four tensors, 0.6 GB: 4.6 TB/s) and 405 us (cut in three; 1.6 GB, and 0.36 GB again: 4.9 TB/s).  A
-// launch's start and end cost about 10 us.  Called without a pause for seconds the kernel reaches the board's power limit (1000 W; a
-// plain copy takes 550), the clock falls to 1.5 GHz, and the first takes 480 to 500 us.  A chunk takes
-// 3570 cycles: the products one after the other with what they wait for.  What did not help, all measured:
+// Measured on one B200 at 1965 MHz: forward B16 H32 T8192 408 us (2.16 GB: 5.3 TB/s, 81 % of the
+// measured copy), B16 H12 T2048 55 us (3.7 TB/s), B1 H32 T32768, which is cut, 182 us (0.54 GB, and
+// 0.24 GB again for the segments' states: 4.3 TB/s); backward of the latter two 135 us (three passes of
+// four tensors, 0.6 GB: 4.5 TB/s) and 407 us (cut in three; 1.6 GB, and 0.36 GB again: 4.8 TB/s).  A
+// launch's start and end cost about 10 us.  Called without a pause for seconds the kernel reaches the
+// board's power limit (1000 W; a plain copy takes 550), the clock falls to 1.5 GHz, and the first takes
+// 480 to 500 us.  A chunk takes 3620 cycles: the products one after the other with what they wait for.
+// What did not help, all measured:
 // three slots for the tiles at the price of one buffer for y' (444 us, 425 then), a second P in tensor
 // memory, so that the next chunk's is there early, at the price of a state product in 64 columns (457), 28
 // warps with two that issue, a prefetch of the next tiles to L2, y' unrolled.
 //
 // Precision: x, y, w are exact in bf16 and every product accumulates in fp32.  Each summand of
 // an output passes one operand rounded to bf16, P o m or C (2^-8 of it, as coarse as the
-// output's own rounding).  The state is an fp32 result that is carried on: it stays in fp32
+// output's own rounding): an output's error is 2.35e-3 of its size against 1.66e-3 for its own
+// rounding alone.  P o m in two parts (the second over P's columns) left 1.88e-3 and took 478 us
+// where this takes 413, timed in turn; for a second part of C there is no shared memory.  The state is an fp32 result that is carried on: it stays in fp32
 // registers, and the decayed rows y' that enter it are three bf16 numbers, all of fp32 (two
 // would leave 2.5e-6 of the state), cut off rather than rounded, so that an infinity's parts agree.
 #pragma once
