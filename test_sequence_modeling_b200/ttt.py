@@ -677,8 +677,10 @@ def ttt_rope(Q, K, rope, positions=None, first_position=0, inverse=False, Q_out=
         raise ValueError("K_out without K")
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")
-    first = _int32(first_position, "first_position")
-    if positions is not None:
+    first = 0
+    if positions is None:
+        first = _int32(first_position, "first_position")
+    else:
         _ints(positions, "positions", (B, T))
     with _on(stream, Q):
         Q_out = _out_as(Q_out, (B, Hq, T, d), Q, "Q_out")

@@ -25,6 +25,12 @@ def test_first_position_arrives_as_given(rec, first):  # noqa: F811
     assert rec.args("ttt_rope")[4] == first
 
 
+def test_first_position_is_not_looked_at_beside_positions(rec):  # noqa: F811
+    ttt.ttt_rope(torch.zeros(B, H, T, d), None, ttt.Rope(torch.zeros(32)), first_position=2 ** 40,
+                 positions=torch.zeros(B, T, dtype=torch.int32))
+    assert rec.names() == ["ttt_rope"]
+
+
 def test_last_position_is_the_librarys_check():
     """2**31 - T is the last first_position of T tokens; the library refuses the next one on the host."""
     from test_sequence_modeling_b200.build import build
